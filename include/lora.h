@@ -379,6 +379,145 @@ lora_status lora_build_apply_noalloc(const lora_stack *st, void *y, int64_t ldy,
 lora_status lora_build_apply_plan(const lora_stack *st, int64_t n_rows, const lora_segments *seg,
                                   int32_t *n_launches);
 
+/* ------------------------------------------------------- microscaled (MX) */
+
+/*
+ * Base projections with 4-bit weights next to the adapters.  The adapters'
+ * deltas are added onto y = W x (page "Multi-LoRA Serving: one base, many
+ * adapters", section 2: the base GEMM is shared by the whole batch); the calls
+ * below compute that y from a weight held in 4 bits, and produce the two forms
+ * of x that a layer then needs from one pass over the hidden state: x in the
+ * stack's dtype for lora_build_apply, and x in 8-bit blocks for the product.
+ *
+ * Block format (OCP microscaling).  A row is cut along k into blocks of 32
+ * elements that share one power of two:
+ *
+ *      v[i] = element[i] * 2^(scale - 127),   scale an 8-bit exponent (e8m0)
+ *
+ * with elements of 8 bits (e4m3: largest 448) or 4 bits (e2m1: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives).  Quantisation takes, for the largest
+ * magnitude m of a block, scale - 127 = floor(log2 m) - emax (emax 8 for e4m3,
+ * 2 for e2m1; at least -127) and rounds each v * 2^-(scale - 127) to the
+ * nearest element, ties to the even code, beyond the largest to the largest.
+ * A block of zeros has scale 0.  A block that holds an infinity or a NaN has
+ * scale 255 (NaN) and zero elements: all 32 of its values stand for NaN.
+ *
+ * Layout of a matrix [n_rows][k] in blocks (public; activations, and weights
+ * as a checkpoint brings them):
+ *   q   codes, row i at byte i * ldq; e4m3 one byte an element, e2m1 two
+ *       elements a byte, the even one in the low half.  A row holds k rounded
+ *       up to 128 elements (LORA_MX_CODE_BYTES).
+ *   s   scales, one byte a block, row i at byte i * lds.  A row holds k rounded
+ *       up to 512 elements' scales (LORA_MX_SCALE_BYTES).
+ * Codes and scales past k are zero: the calls that write blocks write them,
+ * and lora_mx_linear reads them.  q, s, ldq and lds are multiples of 16.
+ *
+ * Matrices in LORA_F32 or LORA_BF16 follow the conventions at the top (row
+ * strides in elements, multiples of 8; k a multiple of 8; 16-byte aligned).
+ * n_rows 0 checks its arguments' values and does nothing.  All sums are fp32.
+ * Nothing is allocated per call, and every call can be captured in a HIP
+ * graph.  Limits: k <= 2^20 (lora_rmsnorm_mx: 2^16), d <= 2^22, n_rows <
+ * 2^30; beyond them LORA_E_UNSUPPORTED.
+ */
+typedef enum lora_mx_format { LORA_MX_E4M3 = 0, LORA_MX_E2M1 = 1 } lora_mx_format;
+
+#define LORA_MX_CODE_BYTES(k, format) \
+    (((((int64_t)(k) + 127) / 128) * 128) >> ((format) == LORA_MX_E2M1 ? 1 : 0))
+#define LORA_MX_SCALE_BYTES(k) ((((int64_t)(k) + 511) / 512) * 16)
+
+typedef struct lora_mx_weight lora_mx_weight; /* owns one 4-bit weight in HBM */
+
+/*
+ * x [n_rows][ldx] (dtype) -> blocks (q, s) of the given format.
+ * Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_mx_quantize(void *q, int64_t ldq, void *s, int64_t lds, lora_mx_format format,
+                             const void *x, int64_t ldx, lora_dtype dtype, int64_t n_rows,
+                             int64_t k, void *stream);
+
+/*
+ * Blocks (q, s) -> the values they stand for, x [n_rows][ldx] in dtype (exact
+ * in either dtype wherever the value is in its range; columns >= k are not
+ * written).  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_mx_dequantize(void *x, int64_t ldx, lora_dtype dtype, const void *q, int64_t ldq,
+                               const void *s, int64_t lds, lora_mx_format format, int64_t n_rows,
+                               int64_t k, void *stream);
+
+/*
+ * Create a 4-bit weight of d output features and k inputs (multiples of 8), in
+ * e2m1 blocks along k: 17/32 bytes an element.  The physical layout is private
+ * (matrix-core operand order).  It starts empty; a later load replaces the
+ * whole weight, in stream order.  Allocates device memory on the current HIP
+ * device; all later calls must run with that device current.  Reading a
+ * weight changes nothing in it: calls that only read it may overlap.
+ * Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_NOMEM, LORA_E_HIP.
+ */
+lora_status lora_mx_weight_create(lora_mx_weight **out, int64_t d, int64_t k);
+
+/* Free a weight (NULL is accepted); synchronises the device first. */
+lora_status lora_mx_weight_destroy(lora_mx_weight *w);
+
+/*
+ * Quantise a dense weight W [d][ldw] (DEVICE, dtype; row o = output feature)
+ * into w.  Errors: LORA_E_ARG, LORA_E_HIP.
+ */
+lora_status lora_mx_weight_load(lora_mx_weight *w, const void *W, int64_t ldw, lora_dtype dtype,
+                                void *stream);
+
+/*
+ * Load a weight that is already in e2m1 blocks (DEVICE q, s in the layout
+ * above, d rows), bit for bit; what the rows hold past k is ignored.  Errors:
+ * LORA_E_ARG, LORA_E_HIP.
+ */
+lora_status lora_mx_weight_load_packed(lora_mx_weight *w, const void *q, int64_t ldq,
+                                       const void *s, int64_t lds, void *stream);
+
+/*
+ * y = X W^T: y[i][o] = round(sum_b 2^(es + ew) sum_{j in b} X[i][j] W[o][j])
+ * over the blocks b of k, for every row i and o < d; X in blocks (q, s) of
+ * either format, products and sums in fp32 on the matrix cores, one rounding
+ * to dtype.  y [n_rows][ldy] is written, columns >= d are not touched.  A NaN
+ * scale or element makes its row (of X) or column (of W) NaN.  The order of
+ * the sums depends on the shapes alone.  Errors: LORA_E_ARG, LORA_E_EMPTY
+ * (nothing was loaded into w), LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_dtype dtype,
+                           const void *q, int64_t ldq, const void *s, int64_t lds,
+                           lora_mx_format format, int64_t n_rows, void *stream);
+
+/*
+ * Residual addition and RMS norm, with the norm in two forms from one pass:
+ *
+ *      h = x + residual                        (fp32; residual NULL: h = x)
+ *      n = h * (mean_j h_j^2 + eps)^-1/2 * weight
+ *      h_out = round(h),  out = round(n),  (q, s) = n in e4m3 blocks
+ *
+ * each output rounded once from the fp32 h or n.  weight: DEVICE [k], dtype.
+ * out, h_out, and q with s may each be NULL, not all of them.  h_out and out
+ * may be x or residual themselves with the same stride (in place); otherwise
+ * the outputs overlap nothing.  eps >= 0.  A row whose h_j^2 all vanish and
+ * eps == 0 gives NaN.  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
+                            void *h_out, int64_t ldh, const void *x, int64_t ldx,
+                            const void *residual, int64_t ldr, const void *weight, float eps,
+                            lora_dtype dtype, int64_t n_rows, int64_t k, void *stream);
+
+/*
+ * The MLP's gated activation, in two forms from one pass: gu [n_rows][ldg]
+ * holds the gate in columns [0, f) and the up projection in [f, 2f) (the two
+ * slices of a gate/up stack);
+ *
+ *      a = g / (1 + exp(-g)) * u,   out = round(a),  (q, s) = a in e4m3 blocks
+ *
+ * each rounded once from the fp32 a.  out, or q with s, may be NULL, not both.
+ * Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_swiglu_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
+                           const void *gu, int64_t ldg, lora_dtype dtype, int64_t n_rows,
+                           int64_t f, void *stream);
+
 /* --------------------------------------------------------------- residency */
 
 /*

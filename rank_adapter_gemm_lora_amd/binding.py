@@ -15,6 +15,7 @@ import threading
 from .build import LIB_PATH
 
 LORA_F32, LORA_BF16 = 0, 1
+LORA_MX_E4M3, LORA_MX_E2M1 = 0, 1
 LORA_OK, LORA_E_ARG, LORA_E_RANK, LORA_E_SLOT, LORA_E_OCCUPIED, LORA_E_EMPTY = 0, 1, 2, 3, 4, 5
 LORA_E_NOMEM, LORA_E_HIP, LORA_E_BAD_IDS, LORA_E_UNSUPPORTED = 6, 7, 8, 9
 LORA_E_CAPACITY, LORA_E_NOT_FOUND = 10, 11
@@ -33,6 +34,9 @@ EXPORTS = ("lora_stack_create", "lora_stack_destroy", "lora_load_slot", "lora_ev
            "lora_build_segments", "lora_add_shrink",
            "lora_add_expand", "lora_apply", "lora_build_shrink", "lora_build_apply",
            "lora_build_apply_noalloc", "lora_build_apply_plan",
+           "lora_mx_quantize", "lora_mx_dequantize", "lora_mx_weight_create",
+           "lora_mx_weight_destroy", "lora_mx_weight_load", "lora_mx_weight_load_packed",
+           "lora_mx_linear", "lora_rmsnorm_mx", "lora_swiglu_mx",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_register",
            "lora_residency_unregister", "lora_residency_map_batch", "lora_residency_slot_of",
            "lora_residency_stats",
@@ -97,6 +101,16 @@ def load(path: str | None = None):
             "lora_build_apply": [P, P, I64, P, I64, P, I64, P, P],
             "lora_build_apply_noalloc": [P, P, I64, P, I64, P, I64, P, P],
             "lora_build_apply_plan": [P, I64, P, P],
+            "lora_mx_quantize": [P, I64, P, I64, I, P, I64, I, I64, I64, P],
+            "lora_mx_dequantize": [P, I64, I, P, I64, P, I64, I, I64, I64, P],
+            "lora_mx_weight_create": [PP, I64, I64],
+            "lora_mx_weight_destroy": [P],
+            "lora_mx_weight_load": [P, P, I64, I, P],
+            "lora_mx_weight_load_packed": [P, P, I64, P, I64, P],
+            "lora_mx_linear": [P, P, I64, I, P, I64, P, I64, I, I64, P],
+            "lora_rmsnorm_mx": [P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, F, I, I64,
+                                I64, P],
+            "lora_swiglu_mx": [P, I64, P, I64, P, I64, P, I64, I, I64, I64, P],
             "lora_residency_create": [PP, P, I, I, I64, I, P, I, I],
             "lora_residency_destroy": [P],
             "lora_residency_register": [P, I64, I, F, P, P],
@@ -265,6 +279,69 @@ def lora_segments_tile_counts(seg, stream=None):
     _check(load().lora_segments_tile_counts(seg, ctypes.byref(b), ctypes.byref(s),
                                             _stream(stream)), "lora_segments_tile_counts")
     return b.value, s.value
+
+
+def lora_mx_code_bytes(k: int, fmt: int) -> int:
+    """Bytes of one row of k codes (the least ldq)."""
+    return (int(k) + 127) // 128 * 128 >> (1 if fmt == LORA_MX_E2M1 else 0)
+
+
+def lora_mx_scale_bytes(k: int) -> int:
+    """Bytes of one row's scales (the least lds)."""
+    return (int(k) + 511) // 512 * 16
+
+
+def lora_mx_quantize(q: int, ldq: int, s: int, lds: int, fmt: int, x: int, ldx: int, dtype: int,
+                     n_rows: int, k: int, stream=None):
+    _check(load().lora_mx_quantize(q, ldq, s, lds, fmt, x, ldx, dtype, n_rows, k, stream),
+           "lora_mx_quantize")
+
+
+def lora_mx_dequantize(x: int, ldx: int, dtype: int, q: int, ldq: int, s: int, lds: int, fmt: int,
+                       n_rows: int, k: int, stream=None):
+    _check(load().lora_mx_dequantize(x, ldx, dtype, q, ldq, s, lds, fmt, n_rows, k, stream),
+           "lora_mx_dequantize")
+
+
+def lora_mx_weight_create(d: int, k: int):
+    out = ctypes.c_void_p()
+    _check(load().lora_mx_weight_create(ctypes.byref(out), int(d), int(k)),
+           "lora_mx_weight_create")
+    return out
+
+
+def lora_mx_weight_destroy(w):
+    _check(load().lora_mx_weight_destroy(w), "lora_mx_weight_destroy")
+
+
+def lora_mx_weight_load(w, W: int, ldw: int, dtype: int, stream=None):
+    _check(load().lora_mx_weight_load(w, W, ldw, dtype, stream), "lora_mx_weight_load")
+
+
+def lora_mx_weight_load_packed(w, q: int, ldq: int, s: int, lds: int, stream=None):
+    _check(load().lora_mx_weight_load_packed(w, q, ldq, s, lds, stream),
+           "lora_mx_weight_load_packed")
+
+
+def lora_mx_linear(w, y: int, ldy: int, dtype: int, q: int, ldq: int, s: int, lds: int, fmt: int,
+                   n_rows: int, stream=None):
+    _check(load().lora_mx_linear(w, y, ldy, dtype, q, ldq, s, lds, fmt, n_rows, stream),
+           "lora_mx_linear")
+
+
+def lora_rmsnorm_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, h_out: int, ldh: int,
+                    x: int, ldx: int, residual: int, ldr: int, weight: int, eps: float, dtype: int,
+                    n_rows: int, k: int, stream=None):
+    """Pointers of outputs and of the residual may be 0 (not wanted / none)."""
+    _check(load().lora_rmsnorm_mx(out, ldo, q, ldq, s, lds, h_out, ldh, x, ldx, residual, ldr,
+                                  weight, eps, dtype, n_rows, k, stream), "lora_rmsnorm_mx")
+
+
+def lora_swiglu_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, gu: int, ldg: int,
+                   dtype: int, n_rows: int, f: int, stream=None):
+    """out, or q with s, may be 0 (not wanted)."""
+    _check(load().lora_swiglu_mx(out, ldo, q, ldq, s, lds, gu, ldg, dtype, n_rows, f, stream),
+           "lora_swiglu_mx")
 
 
 def lora_residency_create(stack, max_cpu_adapters: int, n_slots: int = 0, r_max: int = 0,

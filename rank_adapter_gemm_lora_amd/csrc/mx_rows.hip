@@ -1,0 +1,350 @@
+// mx_rows.hip -- the row-wise microscaled operators: quantisation and its
+// inverse, the weight image, the gated activation and the RMS norm with their
+// block outputs.  All are bound by HBM traffic: each input element is read
+// once and each output written once.
+#include "mx_device.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// x -> blocks.  Per element: the input's 2 or 4 bytes in, 33/32 (e4m3) or
+// 17/32 (e2m1) bytes out.
+template <int DT, int FMT>
+__global__ __launch_bounds__(kRowThreads) void mx_quantize_kernel(MxRowArgs a)
+{
+    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
+    if (i >= a.n_units)   // whole 16-lane groups: n_units is a multiple of 16
+        return;
+    const uint32_t r = mx_div_of(i, a.div);
+    const int unit = (int)(i - r * a.div.d);
+    const int64_t row = a.row0 + r;
+    float f[8];
+    Vec8<DT> v;
+    v.zero();
+    if ((int64_t)unit * 8 < a.k)
+        v.load(a.x, row * a.ldx + unit * 8);
+    v.to_f32(f);
+    mx_store_unit<FMT>(a.b.q + row * a.b.ldq, a.b.s + row * a.b.lds, unit, (int)a.div.d, f);
+}
+
+// silu(g) * u -> a dense row and blocks.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void swiglu_mx_kernel(MxRowArgs a)
+{
+    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
+    if (i >= a.n_units)
+        return;
+    const uint32_t r = mx_div_of(i, a.div);
+    const int unit = (int)(i - r * a.div.d);
+    const int64_t row = a.row0 + r;
+    const bool in = (int64_t)unit * 8 < a.k;
+    Vec8<DT> vg, vu;
+    vg.zero();
+    vu.zero();
+    if (in) {
+        vg.load(a.x, row * a.ldx + unit * 8);
+        vu.load(a.x, row * a.ldx + a.k + unit * 8);
+    }
+    float g[8], u[8], f[8];
+    vg.to_f32(g);
+    vu.to_f32(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = g[e] / (1.f + expf(-g[e])) * u[e];
+    if (in && a.out)
+        Vec8<DT>::store(a.out, row * a.ldo + unit * 8, f);
+    if (a.b.q)
+        mx_store_unit<LORA_MX_E4M3>(a.b.q + row * a.b.ldq, a.b.s + row * a.b.lds, unit,
+                                    (int)a.div.d, f);
+}
+
+// e4m3 / e2m1 codes of 8 elements -> fp32 (the conversions are exact).
+template <int FMT>
+__device__ __forceinline__ void mx_values(typename MxFmt<FMT>::unit_t c, float (&f)[8])
+{
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    f32x2_t p[4];
+    if constexpr (FMT == LORA_MX_E4M3) {
+        p[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
+        p[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+        p[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
+        p[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+    } else {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 0);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 1);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 3);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        f[2 * m] = p[m].x;
+        f[2 * m + 1] = p[m].y;
+    }
+}
+
+// 2^(sb - 127) as a float; 2^-127 is subnormal, 255 is NaN.
+__device__ __forceinline__ float mx_scale_value(uint32_t sb)
+{
+    return __uint_as_float(sb == 0 ? 0x00400000u : sb == 255 ? 0x7fc00000u : sb << 23);
+}
+
+// blocks -> values
+template <int DT, int FMT>
+__global__ __launch_bounds__(kRowThreads) void mx_dequantize_kernel(MxRowArgs a)
+{
+    const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
+    if (i >= a.n_units)
+        return;
+    const uint32_t r = mx_div_of(i, a.div);
+    const int unit = (int)(i - r * a.div.d);
+    const int64_t row = a.row0 + r;
+    if ((int64_t)unit * 8 >= a.k)
+        return;
+    const auto c = *reinterpret_cast<const typename MxFmt<FMT>::unit_t *>(
+        a.b.q + row * a.b.ldq + (int64_t)unit * MxFmt<FMT>::unit_bytes);
+    const float sc = mx_scale_value(a.b.s[row * a.b.lds + (unit >> 2)]);
+    float f[8];
+    mx_values<FMT>(c, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] *= sc;
+    Vec8<DT>::store(a.out, row * a.ldo + unit * 8, f);
+}
+
+// Dense rows -> weight image: thread = (feature, unit of 8 k).  Runs once per
+// weight, not tuned beyond reading whole 16-byte units.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void mx_image_dense_kernel(const void *src, int64_t ldw,
+                                                                     MxImage w)
+{
+    const int units = w.chunks * 16, groups = (w.chunks + 3) / 4;
+    const int unit = blockIdx.y * kRowThreads + threadIdx.x;
+    const int64_t o = blockIdx.x;
+    if (unit >= units)
+        return;
+    Vec8<DT> v;
+    v.zero();
+    if (o < w.d && (int64_t)unit * 8 < w.k)
+        v.load(src, o * ldw + unit * 8);
+    float f[8];
+    v.to_f32(f);
+    const uint32_t sb = mx_block_scale<LORA_MX_E2M1>(f);
+    const int chunk = unit >> 4, g = (unit >> 2) & 3, lane = 16 * g + (int)(o & 15);
+    const int64_t tile = o >> 4;
+    *reinterpret_cast<uint32_t *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16 +
+                                  4 * (unit & 3)) = mx_codes<LORA_MX_E2M1>(f, sb);
+    if ((unit & 3) == 0) {
+        uint8_t *sc = w.scales + ((tile * groups + (chunk >> 2)) * 64 + lane) * 4;
+        sc[chunk & 3] = (uint8_t)sb;
+        if (chunk == w.chunks - 1)
+            for (int j = w.chunks; j < groups * 4; ++j)
+                sc[j & 3] = 0;
+    }
+}
+
+// Rows in e2m1 blocks -> weight image: thread = (feature, block of 32).  Codes
+// and scales past k are replaced by zeros (k is a multiple of 8: whole words).
+__global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b, MxImage w)
+{
+    const int blocks = w.chunks * 4, groups = (w.chunks + 3) / 4;
+    const int blk = blockIdx.y * kRowThreads + threadIdx.x;
+    const int64_t o = blockIdx.x;
+    if (blk >= blocks)
+        return;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t sb = 0;
+    const int64_t k0 = (int64_t)blk * 32;
+    if (o < w.d && k0 < w.k) {
+        c = *reinterpret_cast<const uint4 *>(b.q + o * b.ldq + (int64_t)blk * 16);
+        sb = b.s[o * b.lds + blk];
+        c.y = k0 + 8 < w.k ? c.y : 0u;
+        c.z = k0 + 16 < w.k ? c.z : 0u;
+        c.w = k0 + 24 < w.k ? c.w : 0u;
+    }
+    const int chunk = blk >> 2, lane = 16 * (blk & 3) + (int)(o & 15);
+    const int64_t tile = o >> 4;
+    *reinterpret_cast<uint4 *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16) = c;
+    uint8_t *sc = w.scales + ((tile * groups + (chunk >> 2)) * 64 + lane) * 4;
+    sc[chunk & 3] = (uint8_t)sb;
+    if (chunk == w.chunks - 1)
+        for (int j = w.chunks; j < groups * 4; ++j)
+            sc[j & 3] = 0;
+}
+
+// One row per workgroup of T threads; the row stays in registers, NU units of 8
+// a thread (unit t + T j), so x and the residual are read once and nothing is
+// written before the whole row is in.
+template <int DT, int NU, int T>
+__global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
+{
+    __shared__ float part[T / 64];
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const int units = (int)((a.k + kMxChunk - 1) / kMxChunk) * (kMxChunk / 8);
+    Vec8<DT> vx[NU], vr[NU];
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+        const int64_t c = (int64_t)(tid + T * j) * 8;
+        vx[j].zero();
+        vr[j].zero();
+        if (c < a.k) {
+            vx[j].load(a.x, row * a.ldx + c);
+            if (a.res)
+                vr[j].load(a.res, row * a.ldr + c);
+        }
+    }
+    float f[NU][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+        float r[8];
+        vx[j].to_f32(f[j]);
+        vr[j].to_f32(r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[j][e] += r[e];
+            sum = fmaf(f[j][e], f[j][e], sum);
+        }
+    }
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1)
+        sum += __shfl_xor(sum, m);
+    if (T > 64) {
+        if ((tid & 63) == 0)
+            part[tid >> 6] = sum;
+        __syncthreads();
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w)
+            sum += part[w];
+    }
+    const float inv = 1.f / sqrtf(sum / (float)a.k + a.eps);
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+        const int unit = tid + T * j;
+        const int64_t c = (int64_t)unit * 8;
+        if (c < a.k) {
+            if (a.h)
+                Vec8<DT>::store(a.h, row * a.ldh + c, f[j]);
+            Vec8<DT> vw;
+            vw.load(a.weight, c);
+            float w[8];
+            vw.to_f32(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[j][e] = f[j][e] * inv * w[e];
+            if (a.out)
+                Vec8<DT>::store(a.out, row * a.ldo + c, f[j]);
+        }
+        if (a.b.q && unit < units)   // whole 16-lane groups
+            mx_store_unit<LORA_MX_E4M3>(a.b.q + row * a.b.ldq, a.b.s + row * a.b.lds, unit, units,
+                                        f[j]);
+    }
+}
+
+// Launch `go` over slabs of rows whose units fit 31 bits.
+template <class F> hipError_t by_slabs(MxRowArgs a, int64_t n_rows, F go)
+{
+    const int64_t units = (a.k + kMxChunk - 1) / kMxChunk * (kMxChunk / 8);
+    a.div = mx_div((uint32_t)units);
+    const int64_t most = ((int64_t)1 << 30) / units;
+    for (int64_t r = 0; r < n_rows; r += most) {
+        a.row0 = r;
+        a.n_units = (uint32_t)((n_rows - r < most ? n_rows - r : most) * units);
+        go(a, dim3((a.n_units + kRowThreads - 1) / kRowThreads));
+    }
+    return hipGetLastError();
+}
+
+template <int DT, int NU, int T> void norm_go(const MxNormArgs &a, hipStream_t s)
+{
+    rmsnorm_mx_kernel<DT, NU, T><<<dim3((uint32_t)a.n_rows), dim3(T), 0, s>>>(a);
+}
+
+template <int DT> void norm_pick(const MxNormArgs &a, hipStream_t s)
+{
+    const int64_t units = (a.k + 7) / 8;
+    if (units <= 64)
+        norm_go<DT, 1, 64>(a, s);
+    else if (units <= 256)
+        norm_go<DT, 1, 256>(a, s);
+    else if (units <= 512)
+        norm_go<DT, 2, 256>(a, s);
+    else if (units <= 1024)
+        norm_go<DT, 4, 256>(a, s);
+    else if (units <= 2048)
+        norm_go<DT, 4, 512>(a, s);
+    else if (units <= 4096)
+        norm_go<DT, 4, 1024>(a, s);
+    else
+        norm_go<DT, 8, 1024>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(int dtype, int format, MxRowArgs a, int64_t n_rows, hipStream_t s)
+{
+    return by_slabs(a, n_rows, [&](const MxRowArgs &b, dim3 grid) {
+        if (dtype == DT_F32 && format == LORA_MX_E4M3)
+            mx_quantize_kernel<DT_F32, LORA_MX_E4M3><<<grid, kRowThreads, 0, s>>>(b);
+        else if (dtype == DT_F32)
+            mx_quantize_kernel<DT_F32, LORA_MX_E2M1><<<grid, kRowThreads, 0, s>>>(b);
+        else if (format == LORA_MX_E4M3)
+            mx_quantize_kernel<DT_BF16, LORA_MX_E4M3><<<grid, kRowThreads, 0, s>>>(b);
+        else
+            mx_quantize_kernel<DT_BF16, LORA_MX_E2M1><<<grid, kRowThreads, 0, s>>>(b);
+    });
+}
+
+hipError_t launch_mx_dequantize(int dtype, int format, MxRowArgs a, int64_t n_rows, hipStream_t s)
+{
+    return by_slabs(a, n_rows, [&](const MxRowArgs &b, dim3 grid) {
+        if (dtype == DT_F32 && format == LORA_MX_E4M3)
+            mx_dequantize_kernel<DT_F32, LORA_MX_E4M3><<<grid, kRowThreads, 0, s>>>(b);
+        else if (dtype == DT_F32)
+            mx_dequantize_kernel<DT_F32, LORA_MX_E2M1><<<grid, kRowThreads, 0, s>>>(b);
+        else if (format == LORA_MX_E4M3)
+            mx_dequantize_kernel<DT_BF16, LORA_MX_E4M3><<<grid, kRowThreads, 0, s>>>(b);
+        else
+            mx_dequantize_kernel<DT_BF16, LORA_MX_E2M1><<<grid, kRowThreads, 0, s>>>(b);
+    });
+}
+
+hipError_t launch_swiglu_mx(int dtype, MxRowArgs a, int64_t n_rows, hipStream_t s)
+{
+    return by_slabs(a, n_rows, [&](const MxRowArgs &b, dim3 grid) {
+        if (dtype == DT_F32)
+            swiglu_mx_kernel<DT_F32><<<grid, kRowThreads, 0, s>>>(b);
+        else
+            swiglu_mx_kernel<DT_BF16><<<grid, kRowThreads, 0, s>>>(b);
+    });
+}
+
+hipError_t launch_rmsnorm_mx(int dtype, const MxNormArgs &a, hipStream_t s)
+{
+    if (dtype == DT_F32)
+        norm_pick<DT_F32>(a, s);
+    else
+        norm_pick<DT_BF16>(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_image(int dtype, const void *src, int64_t ldw, const MxBlocks &b,
+                           const MxImage &w, hipStream_t s)
+{
+    const uint32_t rows = (uint32_t)w.tiles * 16;
+    const uint32_t per = dtype < 0 ? w.chunks * 4 : w.chunks * 16;
+    const dim3 grid(rows, (per + kRowThreads - 1) / kRowThreads);
+    if (dtype < 0)
+        mx_image_packed_kernel<<<grid, kRowThreads, 0, s>>>(b, w);
+    else if (dtype == DT_F32)
+        mx_image_dense_kernel<DT_F32><<<grid, kRowThreads, 0, s>>>(src, ldw, w);
+    else
+        mx_image_dense_kernel<DT_BF16><<<grid, kRowThreads, 0, s>>>(src, ldw, w);
+    return hipGetLastError();
+}
+
+}  // namespace lora
