@@ -77,8 +77,11 @@ hipError_t launch_rmsnorm_mx(int dtype, const MxNormArgs &a, hipStream_t s);
 
 // The weight image.  Output features are cut into tiles of 16, k into chunks of
 // 128; per (tile, chunk) the codes are one kilobyte in matrix-core operand
-// order: lane l = 16 g + m holds feature m's 32 codes of k 32 g .. + 31 (16
-// bytes), which is block g of the chunk.  The scales of four chunks are 256
+// order: lane l = 16 g + r holds the 32 codes of k 32 g .. + 31 (16 bytes) of
+// the feature in row r, which is block g of the chunk.  A pair of tiles shares
+// 32 features: row 4 g + i of tile 2 p + h is feature 32 p + 8 g + 4 h + i, so
+// that the lane that gets rows 4 g .. + 3 of both tiles' results has eight
+// neighbouring features of a row.  The scales of four chunks are 256
 // bytes: byte j of lane l's word is the scale of that lane's block in chunk j.
 // Both are padded with zeros: features to kMxPadRows, scales to four chunks.
 struct MxImage {

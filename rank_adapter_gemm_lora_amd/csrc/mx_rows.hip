@@ -114,6 +114,10 @@ __global__ __launch_bounds__(kRowThreads) void mx_dequantize_kernel(MxRowArgs a)
     Vec8<DT>::store(a.out, row * a.ldo + unit * 8, f);
 }
 
+// Where the image keeps output feature o.
+__device__ __forceinline__ int64_t mx_image_tile(int64_t o) { return (o >> 5) * 2 + ((o >> 2) & 1); }
+__device__ __forceinline__ int mx_image_row(int64_t o) { return (int)(((o >> 3) & 3) * 4 + (o & 3)); }
+
 // Dense rows -> weight image: thread = (feature, unit of 8 k).  Runs once per
 // weight, not tuned beyond reading whole 16-byte units.
 template <int DT>
@@ -132,8 +136,8 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_dense_kernel(const void 
     float f[8];
     v.to_f32(f);
     const uint32_t sb = mx_block_scale<LORA_MX_E2M1>(f);
-    const int chunk = unit >> 4, g = (unit >> 2) & 3, lane = 16 * g + (int)(o & 15);
-    const int64_t tile = o >> 4;
+    const int chunk = unit >> 4, lane = 16 * ((unit >> 2) & 3) + mx_image_row(o);
+    const int64_t tile = mx_image_tile(o);
     *reinterpret_cast<uint32_t *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16 +
                                   4 * (unit & 3)) = mx_codes<LORA_MX_E2M1>(f, sb);
     if ((unit & 3) == 0) {
@@ -164,8 +168,8 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b
         c.z = k0 + 16 < w.k ? c.z : 0u;
         c.w = k0 + 24 < w.k ? c.w : 0u;
     }
-    const int chunk = blk >> 2, lane = 16 * (blk & 3) + (int)(o & 15);
-    const int64_t tile = o >> 4;
+    const int chunk = blk >> 2, lane = 16 * (blk & 3) + mx_image_row(o);
+    const int64_t tile = mx_image_tile(o);
     *reinterpret_cast<uint4 *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16) = c;
     uint8_t *sc = w.scales + ((tile * groups + (chunk >> 2)) * 64 + lane) * 4;
     sc[chunk & 3] = (uint8_t)sb;
