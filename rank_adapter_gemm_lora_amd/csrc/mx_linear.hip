@@ -21,6 +21,7 @@
 // what the four bf16 instructions on widened codes do, at a quarter of the LDS
 // traffic and with no widening of W.
 #include <type_traits>
+#include <utility>
 
 #include "mx_device.h"
 
@@ -38,24 +39,27 @@ constexpr int kFp8 = 0, kFp4 = 4;   // operand format codes of the instruction
 template <int FMT> struct MxOperand;
 template <> struct MxOperand<LORA_MX_E2M1> {
     i32x8_t v;
-    __device__ __forceinline__ explicit MxOperand(u32x4_t c)
-        : v{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0}
+    __device__ __forceinline__ void set(u32x4_t c, u32x4_t)
     {
+        v = i32x8_t{(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
     }
 };
 template <> struct MxOperand<LORA_MX_E4M3> {
-    i32x8_t hi, lo;   // codes of |x| >= 2 and of the rest, zeros in the other's places
-    __device__ __forceinline__ MxOperand(u32x4_t a, u32x4_t b)
+    i32x8_t v, lo;   // codes of |x| >= 2 and of the rest, zeros in the other's places
+    __device__ __forceinline__ void set_word(int i, u32x4_t a, u32x4_t b)
     {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t c = i < 4 ? a[i & 3] : b[i & 3];
+        // byte masks from bit 6: moved to the sign of bytes 1, 3, 5 and 7,
+        // which selectors 8 .. 11 of the byte permutation spread
+        const uint32_t h = c & __builtin_amdgcn_perm(c << 1, c << 9, 0x0b090a08u);
+        v[i] = (int)h;
+        lo[i] = (int)(c ^ h);
+    }
+    __device__ __forceinline__ void set(u32x4_t a, u32x4_t b)
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // byte masks from bit 6: moved to the sign of bytes 1, 3, 5 and 7,
-            // which selectors 8 .. 11 of the byte permutation spread
-            const uint32_t h = w[i] & __builtin_amdgcn_perm(w[i] << 1, w[i] << 9, 0x0b090a08u);
-            hi[i] = (int)h;
-            lo[i] = (int)(w[i] ^ h);
-        }
+        for (int i = 0; i < 8; ++i)
+            set_word(i, a, b);
     }
 };
 
@@ -88,109 +92,177 @@ __device__ __forceinline__ void mx_store8(void *y, int64_t idx, f32x4_t u, f32x4
     Vec8<DT>::store(y, idx, f);
 }
 
-// ---------------------------------------------------------------- few rows
+template <class F, int... I> __device__ __forceinline__ void mx_for(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void mx_for(F f)
+{
+    mx_for(f, std::make_integer_sequence<int, N>{});
+}
+
+// ------------------------------------------------------ few rows, small grids
 //
-// One workgroup: 16 features x 16 MT rows; its NW wavefronts take groups of
-// four chunks in turn and are summed in wavefront order through LDS.  W is
-// streamed once, straight into registers in operand order; all of a group's
-// loads are issued before its first product, and the next group's before that.
-template <int FMT, int MT> struct MxGroup {
-    u32x4_t w[4];
-    uint32_t sw;
-    u32x4_t x[MT][4][FMT == LORA_MX_E4M3 ? 2 : 1];
-    u32x4_t sx[MT];
-    // wc, ws: this lane's words of the tile; xq, xs: its rows
-    __device__ __forceinline__ void load(int grp, int chunks, const uint8_t *wc, const uint8_t *ws,
-                                         const uint8_t *const (&xq)[MT], const uint8_t *const (&xs)[MT])
-    {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = min(4 * grp + j, chunks - 1);   // past the end: not multiplied
-            w[j] = *reinterpret_cast<const u32x4_t *>(wc + c * 1024);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                x[t][j][0] = *reinterpret_cast<const u32x4_t *>(
-                    xq[t] + c * (FMT == LORA_MX_E4M3 ? 128 : 64));
-                if constexpr (FMT == LORA_MX_E4M3)
-                    x[t][j][1] = *reinterpret_cast<const u32x4_t *>(xq[t] + c * 128 + 64);
-            }
-        }
-        sw = *reinterpret_cast<const uint32_t *>(ws + (int64_t)grp * 256);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-            sx[t] = *reinterpret_cast<const u32x4_t *>(xs[t] + (int64_t)grp * 16);
-    }
-    template <int J>
-    __device__ __forceinline__ void chunk(int g, f32x4_t (&acc)[MT])
-    {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const uint32_t s4 = J == 0 ? sx[t].x : J == 1 ? sx[t].y : J == 2 ? sx[t].z : sx[t].w;
-            const uint32_t s = s4 >> (8 * g);
-            if constexpr (FMT == LORA_MX_E4M3) {
-                const MxOperand<FMT> o(x[t][J][0], x[t][J][1]);
-                acc[t] = mx_mfma<FMT, J>(w[J], sw, o.hi, s, acc[t]);
-                acc[t] = mx_mfma<FMT, J>(w[J], sw, o.lo, s, acc[t]);
-            } else {
-                acc[t] = mx_mfma<FMT, J>(w[J], sw, MxOperand<FMT>(x[t][J][0]).v, s, acc[t]);
-            }
-        }
-    }
-    __device__ __forceinline__ void multiply(int n, int g, f32x4_t (&acc)[MT])
-    {
-        chunk<0>(g, acc);
-        if (n > 1)
-            chunk<1>(g, acc);
-        if (n > 2)
-            chunk<2>(g, acc);
-        if (n > 3)
-            chunk<3>(g, acc);
-    }
+// One workgroup: 16 MT rows x 16 NT features; its wavefronts take groups of
+// four chunks in turn, each for the whole tile, and are summed in wavefront
+// order through LDS.  Operands go straight into registers (W in operand order,
+// X as 16 rows' pieces of 16 bytes): nothing is shared between wavefronts, so
+// there is no LDS traffic and no barrier in the loop.  A wavefront holds four
+// chunks; each is refilled with the next group's as soon as it is multiplied.
+constexpr int kDirectWaves = 8;
+
+template <int FMT, int MT, int NT> struct MxChunk {
+    u32x4_t w[NT], x[MT][FMT == LORA_MX_E4M3 ? 2 : 1];
 };
 
-template <int DT, int FMT, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void mx_linear_few_kernel(MxLinearArgs a)
+template <int DT, int FMT, int MT, int NT>
+__global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(MxLinearArgs a, int row_tiles, int col_tiles)
 {
-    __shared__ f32x4_t part[NW][MT][64];
+    constexpr int NW = kDirectWaves;
+    constexpr int kPair = NT > 1 ? 2 : 1, kParts = MT * NT / kPair;
+    __shared__ f32x4_t part[NW][MT * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const int64_t tile = blockIdx.x;
-    const int64_t row0 = (int64_t)blockIdx.y * (16 * MT);
+    const int id = xcd_major(blockIdx.x, gridDim.x);
+    const int band = id / (8 * col_tiles), in = id % (8 * col_tiles);
+    const int tall = min(8, row_tiles - 8 * band);
+    const int64_t row0 = (int64_t)(8 * band + in % tall) * (16 * MT);
+    const int64_t tile0 = (int64_t)(in / tall) * NT;
     const int chunks = a.w.chunks, groups = (chunks + 3) / 4;
-    const uint8_t *wc = a.w.codes + (tile * chunks * 64 + lane) * 16;
-    const uint8_t *ws = a.w.scales + (tile * groups * 64 + lane) * 4;
-    const uint8_t *xq[MT], *xs[MT];
-    f32x4_t acc[MT];
+    const uint8_t *xq[MT], *xs[MT], *wc[NT];
+    f32x4_t acc[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        int64_t r = row0 + 16 * t + m;   // rows past the end repeat the last one
-        r = r < a.n_rows ? r : a.n_rows - 1;
+        const int64_t r = min(row0 + 16 * t + m, a.n_rows - 1);   // rows past the end repeat the last one
         xq[t] = a.q + r * a.ldq + 16 * g;
         xs[t] = a.s + r * a.lds;
-        acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    MxGroup<FMT, MT> cur, nxt;
-    if (wave < groups)
-        cur.load(wave, chunks, wc, ws, xq, xs);
-    for (int grp = wave; grp < groups; grp += NW) {
-        if (grp + NW < groups)
-            nxt.load(grp + NW, chunks, wc, ws, xq, xs);
-        cur.multiply(chunks - 4 * grp, g, acc);
-        cur = nxt;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            acc[t][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-        part[wave][t][lane] = acc[t];
+    for (int n = 0; n < NT; ++n)
+        wc[n] = a.w.codes + ((tile0 + n) * chunks * 64 + lane) * 16;
+    const uint8_t *ws = a.w.scales + (tile0 * groups * 64 + lane) * 4;
+
+    MxChunk<FMT, MT, NT> ring[4];
+    u32x4_t sx[MT], sxn[MT];
+    uint32_t sw[NT], swn[NT];
+    auto load = [&](auto J, int grp) {
+        constexpr int j = decltype(J)::value;
+        // past the end: the last chunk again, not multiplied
+        const int64_t c = min(4 * grp + j, chunks - 1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            ring[j].w[n] = *reinterpret_cast<const u32x4_t *>(wc[n] + c * 1024);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            ring[j].x[t][0] = *reinterpret_cast<const u32x4_t *>(xq[t] + c * (FMT == LORA_MX_E4M3 ? 128 : 64));
+            if constexpr (FMT == LORA_MX_E4M3)
+                ring[j].x[t][1] = *reinterpret_cast<const u32x4_t *>(xq[t] + c * 128 + 64);
+        }
+    };
+    auto load_scales = [&](int grp) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            sxn[t] = *reinterpret_cast<const u32x4_t *>(xs[t] + (int64_t)grp * 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            swn[n] = *reinterpret_cast<const uint32_t *>(ws + ((int64_t)n * groups + grp) * 256);
+    };
+    auto take_scales = [&]() {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            sx[t] = sxn[t];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            sw[n] = swn[n];
+    };
+    // products of one chunk; the next X tile's codes are split between them
+    auto multiply = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        MxOperand<FMT> x, next;
+        auto tile = [&](MxOperand<FMT> &o, int t, int i) {
+            if constexpr (FMT == LORA_MX_E4M3)
+                o.set_word(i, ring[j].x[t][0], ring[j].x[t][1]);
+            else if (i == 0)
+                o.set(ring[j].x[t][0], ring[j].x[t][0]);
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            tile(x, 0, i);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const uint32_t s = sx[t][j] >> (8 * g);
+            constexpr int kParts = FMT == LORA_MX_E4M3 ? 2 * NT : NT;
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                if constexpr (FMT == LORA_MX_E4M3)
+                    acc[t][n % NT] = mx_mfma<FMT, j>(ring[j].w[n % NT], sw[n % NT], n < NT ? x.v : x.lo, s, acc[t][n % NT]);
+                else
+                    acc[t][n] = mx_mfma<FMT, j>(ring[j].w[n], sw[n], x.v, s, acc[t][n]);
+                if (t + 1 < MT) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 8 * n / kParts; i < 8 * (n + 1) / kParts; ++i)
+                        tile(next, t + 1, i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            x = next;
+        }
+    };
+    int grp = wave;
+    if (grp < groups) {
+        load_scales(grp);
+        mx_for<4>([&](auto J) { load(J, grp); });
+        for (; grp + NW < groups; grp += NW) {
+            take_scales();
+            load_scales(grp + NW);
+            mx_for<4>([&](auto J) {
+                multiply(J);
+                load(J, grp + NW);
+            });
+        }
+        take_scales();
+        mx_for<4>([&](auto J) {
+            if (4 * grp + decltype(J)::value < chunks)
+                multiply(J);
+        });
+    }
+    // wavefront p % NW finishes part p: it keeps its own sums of it
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+        if (p % NW == wave)
+            continue;
+#pragma unroll
+        for (int i = kPair * p; i < kPair * (p + 1); ++i)
+            part[wave][i][lane] = acc[i / NT][i % NT];
+    }
     __syncthreads();
-    for (int t = wave; t < MT; t += NW) {
-        f32x4_t v = part[0][t][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w)
-            v += part[w][t][lane];
-        const int64_t r = row0 + 16 * t + m;
-        const int64_t o = (tile >> 1) * 32 + 8 * g + 4 * (tile & 1);
-        if (r < a.n_rows && o < a.w.d)
-            mx_store4<DT>(a.y, r * a.ldy + o, v);
+    for (int p = 0; p < kParts; ++p) {
+        if (p % NW != wave)
+            continue;
+        f32x4_t v[kPair];
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) {
+            const int f = kPair * p + i;
+            v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                v[i] += w == p % NW ? acc[f / NT][f % NT] : part[w][f][lane];
+        }
+        const int64_t r = row0 + 16 * (kPair * p / NT) + m;
+        if constexpr (kPair == 2) {
+            const int64_t o = (tile0 + kPair * p % NT) * 16 + 8 * g;
+            if (r < a.n_rows && o < a.w.d)
+                mx_store8<DT>(a.y, r * a.ldy + o, v[0], v[1]);
+        } else {
+            const int64_t o = (tile0 >> 1) * 32 + 8 * g + 4 * (tile0 & 1);
+            if (r < a.n_rows && o < a.w.d)
+                mx_store4<DT>(a.y, r * a.ldy + o, v[0]);
+        }
     }
 }
 
@@ -221,10 +293,12 @@ struct MxTile {
     static constexpr int kWUnits = kTiles * kSC * 64;
     static constexpr int kXCopies = kXUnits / 64 / kSet;      // of a wavefront, a stage
     static constexpr int kWCopies = kWUnits / 64 / kSet;
+    static constexpr int kXScaleCopies = kRows / 64;          // of the set, four chunks
+    static constexpr int kScaleCopies = kXScaleCopies + kTiles / 4;
     static_assert(kXUnits % (64 * kSet) == 0 && kWUnits % (64 * kSet) == 0, "whole copies");
+    static_assert(kRows % 64 == 0 && kTiles % 4 == 0, "whole copies of scales");
     static_assert(NT % 2 == 0, "features come in pairs of tiles");
-    static_assert(KW == 1 || (MT % 2 == 0 && KW / 2 * kSet * MT / 2 * NT * 64 <= KW * kXUnits),
-                  "half the sets' sums fit the X slots, even row tiles one and odd ones the other");
+    static_assert(KW == 1 || FW * NT <= 8, "half the sets' sums fit the X slots, even tiles one and odd ones the other");
 };
 
 __device__ __forceinline__ void mx_copy16(const uint8_t *src, u32x4_t *dst)
@@ -240,6 +314,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     typedef MxTile<DT, FMT, RW, MT, FW, NT, KW> T;
     __shared__ u32x4_t x0[KW * T::kXUnits], x1[KW * T::kXUnits];
     __shared__ u32x4_t w0[KW * T::kWUnits], w1[KW * T::kWUnits];
+    __shared__ u32x4_t scales[KW * T::kScaleCopies * 64];   // of four chunks: X rows, W tiles
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int set = wave / T::kSet, wv = wave % T::kSet;
@@ -267,13 +342,19 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         xsrc[i] = a.q + row * a.ldq;
     }
     const uint8_t *wsrc = a.w.codes + tile0 * chunks * 1024 + lane * 16;
-    const uint8_t *xss[MT];
+    // a set's copies of scales are dealt out to its wavefronts
+    constexpr int kDeal = (T::kScaleCopies + T::kSet - 1) / T::kSet;
+    const uint8_t *ssrc[kDeal];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-        xss[t] = a.s + min(row0 + 16 * (wr * MT + t) + m, a.n_rows - 1) * a.lds;
-    const uint8_t *wss = a.w.scales + (tile0 + wf * NT) * groups * 256 + lane * 4;
+    for (int i = 0; i < kDeal; ++i) {
+        const int n = i * T::kSet + wv;   // X: a row a lane; W: four tiles of 16 lanes
+        const int64_t row = min(row0 + 64 * n + lane, a.n_rows - 1);
+        const int64_t tile = tile0 + 4 * (n - T::kXScaleCopies) + (lane >> 4);
+        ssrc[i] = n < T::kXScaleCopies ? a.s + row * a.lds : a.w.scales + tile * groups * 256 + (lane & 15) * 16;
+    }
 
-    uint32_t sx[MT][T::kSC], sxn[MT][T::kSC], sw[NT], swn[NT];
+    u32x4_t sx[MT];
+    uint32_t sw[NT];
     f32x4_t acc[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -281,8 +362,8 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         for (int n = 0; n < NT; ++n)
             acc[t][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // copies of the stage that starts at chunk c, and its scales into registers
-    auto fetch = [&](int c, u32x4_t *xd, u32x4_t *wd, bool group) {
+    // copies of the stage that starts at chunk c
+    auto fetch = [&](int c, u32x4_t *xd, u32x4_t *wd) {
         const bool half = FMT == LORA_MX_E2M1 && c + 1 >= chunks;   // the row ends inside the stage
 #pragma unroll
         for (int i = 0; i < T::kXCopies; ++i) {
@@ -296,42 +377,67 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
             mx_copy16(wsrc + ((int64_t)tile * chunks + min(c + h, chunks - 1)) * 1024,
                       wd + set * T::kWUnits + b * 64);
         }
+    };
+    auto fetch_scales = [&](int grp) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int h = 0; h < T::kSC; ++h)
-                sxn[t][h] = *reinterpret_cast<const uint32_t *>(xss[t] + 4 * (c + h));
-        if (group) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                swn[n] = *reinterpret_cast<const uint32_t *>(wss + ((int64_t)n * groups + (c >> 2)) * 256);
+        for (int i = 0; i < kDeal; ++i) {
+            const int n = i * T::kSet + wv;
+            if (n < T::kScaleCopies)
+                mx_copy16(ssrc[i] + (int64_t)grp * (n < T::kXScaleCopies ? 16 : 256),
+                          scales + (set * T::kScaleCopies + n) * 64);
         }
     };
-    // one chunk, H the half of its stage
-    auto multiply = [&](auto J, auto H, const u32x4_t *xd, const u32x4_t *wd) {
-        constexpr int j = decltype(J)::value, h = decltype(H)::value;
+    // One chunk, H the half of its stage: the W tiles' codes and the first X
+    // tile's are read (load), then multiplied tile by tile (multiply), each X
+    // tile read one ahead; the split of the next X tile's codes is spread over
+    // the products of this one's lower part.
+    u32x4_t w[NT], xa, xb;
+    auto read_x = [&](int t, int h, const u32x4_t *xd) {
+        const u32x4_t *xp = xd + set * T::kXUnits + (wr * MT * 16 + 16 * t + m) * 8;
+        if constexpr (FMT == LORA_MX_E4M3) {
+            xa = xp[g ^ (m >> 1)];
+            xb = xp[(4 + g) ^ (m >> 1)];
+        } else {
+            xa = xp[(4 * h + g) ^ (m >> 1)];
+        }
+    };
+    auto load = [&](int h, const u32x4_t *xd, const u32x4_t *wd) {
         const u32x4_t *wp = wd + set * T::kWUnits + (h * T::kTiles + wf * NT) * 64 + lane;
-        const u32x4_t *xp = xd + set * T::kXUnits + (wr * MT * 16 + m) * 8;
-        u32x4_t w[NT];
+        read_x(0, h, xd);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             w[n] = wp[64 * n];
+    };
+    auto multiply = [&](auto J, int h, const u32x4_t *xd) {
+        constexpr int j = decltype(J)::value;
+        MxOperand<FMT> x, next;
+        x.set(xa, xb);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const uint32_t s = sx[t][h] >> (8 * g);
+            const uint32_t s = sx[t][j] >> (8 * g);
+            if (t + 1 < MT)
+                read_x(t + 1, h, xd);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], x.v, s, acc[t][n]);
             if constexpr (FMT == LORA_MX_E4M3) {
-                const MxOperand<FMT> o(xp[128 * t + (g ^ (m >> 1))], xp[128 * t + ((4 + g) ^ (m >> 1))]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], o.hi, s, acc[t][n]);
+                for (int n = 0; n < NT; ++n) {
+                    acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], x.lo, s, acc[t][n]);
+                    if (t + 1 < MT) {
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], o.lo, s, acc[t][n]);
-            } else {
-                const MxOperand<FMT> o(xp[128 * t + ((4 * h + g) ^ (m >> 1))]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], o.v, s, acc[t][n]);
+                        for (int i = 8 * n / NT; i < 8 * (n + 1) / NT; ++i)
+                            next.set_word(i, xa, xb);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                x = next;
+                __builtin_amdgcn_s_setprio(0);
+            } else if (t + 1 < MT) {
+                x.set(xa, xb);
             }
         }
     };
@@ -341,26 +447,45 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         u32x4_t *xn = st & 1 ? x0 : x1, *wn = st & 1 ? w0 : w1;
         __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt 0, lgkmcnt 0
         asm volatile("s_barrier" ::: "memory");
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int h = 0; h < T::kSC; ++h)
-                sx[t][h] = sxn[t][h];
         if constexpr (st == 0) {
+            // this group's scales; their slot is refilled behind the next barrier
+            const u32x4_t *sp = scales + set * T::kScaleCopies * 64;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                sx[t] = sp[16 * (wr * MT + t) + m];
+            const uint32_t *swp = reinterpret_cast<const uint32_t *>(sp + T::kXScaleCopies * 64);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                sw[n] = swn[n];
+                sw[n] = swp[64 * (wf * NT + n) + lane];
+        }
+        // With several row tiles a wavefront, this stage's first operands are on
+        // their way while the next stage's copies are issued; with one the
+        // stages are short, and the copies go first.
+        if constexpr (MT > 1) {
+            load(0, xc, wc);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (c + T::kSC < c_end)
-            fetch(c + T::kSC, xn, wn, (st + 1) * T::kSC == 4);
+            fetch(c + T::kSC, xn, wn);
+        if (st == 1 && c + 4 - T::kSC < c_end)
+            fetch_scales((c - T::kSC) / 4 + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MT == 1)
+            load(0, xc, wc);
         if (c < c_end)
-            multiply(std::integral_constant<int, st * T::kSC>{}, std::integral_constant<int, 0>{}, xc, wc);
-        if constexpr (T::kSC == 2)
-            if (c + 1 < c_end)
-                multiply(std::integral_constant<int, st * 2 + 1>{}, std::integral_constant<int, 1>{}, xc, wc);
+            multiply(std::integral_constant<int, st * T::kSC>{}, 0, xc);
+        if constexpr (T::kSC == 2) {
+            if (c + 1 < c_end) {
+                load(1, xc, wc);
+                multiply(std::integral_constant<int, st * 2 + 1>{}, 1, xc);
+            }
+        }
     };
     if (c_begin < c_end)
-        fetch(c_begin, x0, w0, true);
+    {
+        fetch(c_begin, x0, w0);
+        fetch_scales(c_begin / 4);
+    }
     for (int i = 0; i < per; ++i) {
         const int c = c_begin + 4 * i;
         step(std::integral_constant<int, 0>{}, c);
@@ -376,21 +501,21 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         for (int half = KW / 2; half > 0; half /= 2) {
             __syncthreads();
             if (set >= half && set < 2 * half) {
-                const int at = ((set - half) * T::kSet + wv) * (MT / 2 * NT * 64) + lane;
+                const int at = ((set - half) * T::kSet + wv) * (MT * NT / 2 * 64) + lane;
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        reinterpret_cast<f32x4_t *>(t & 1 ? x1 : x0)[at + (t / 2 * NT + n) * 64] = acc[t][n];
+                        reinterpret_cast<f32x4_t *>(n & 1 ? x1 : x0)[at + (t * NT + n) / 2 * 64] = acc[t][n];
             }
             __syncthreads();
             if (set < half) {
-                const int at = (set * T::kSet + wv) * (MT / 2 * NT * 64) + lane;
+                const int at = (set * T::kSet + wv) * (MT * NT / 2 * 64) + lane;
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        acc[t][n] += reinterpret_cast<const f32x4_t *>(t & 1 ? x1 : x0)[at + (t / 2 * NT + n) * 64];
+                        acc[t][n] += reinterpret_cast<const f32x4_t *>(n & 1 ? x1 : x0)[at + (t * NT + n) / 2 * 64];
             }
         }
         if (set > 0)
@@ -408,38 +533,96 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     }
 }
 
+// Launch `go` over slabs of rows, so that a launch has at most 2^29 tiles.
+template <int DT, class F> void by_row_slabs(const MxLinearArgs &a, int rows, int tiles, F go)
+{
+    const int64_t cols = (a.w.d + 16 * tiles - 1) / (16 * tiles);
+    const int64_t most = ((((int64_t)1 << 29) / cols) & ~(int64_t)7) * rows;
+    for (int64_t r = 0; r < a.n_rows; r += most) {
+        MxLinearArgs b = a;
+        b.n_rows = a.n_rows - r < most ? a.n_rows - r : most;
+        b.q = a.q + r * a.ldq;
+        b.s = a.s + r * a.lds;
+        b.y = static_cast<char *>(a.y) + r * a.ldy * (DT == DT_F32 ? 4 : 2);
+        go(b, (int)((b.n_rows + rows - 1) / rows), (int)cols);
+    }
+}
+
+template <int DT, int FMT, int MT, int NT> void linear_direct(const MxLinearArgs &a, hipStream_t s)
+{
+    // one tile a workgroup: both of every pair
+    constexpr int kPer = NT == 1 ? 2 : 1;
+    by_row_slabs<DT>(a, 16 * MT, NT * kPer, [&](const MxLinearArgs &b, int rows, int cols) {
+        mx_linear_direct_kernel<DT, FMT, MT, NT>
+            <<<dim3((uint32_t)rows * cols * kPer), 64 * kDirectWaves, 0, s>>>(b, rows, cols * kPer);
+    });
+}
+
 template <int DT, int FMT, int RW, int MT, int FW, int NT, int KW>
 void linear_tiles(const MxLinearArgs &a, hipStream_t s)
 {
     typedef MxTile<DT, FMT, RW, MT, FW, NT, KW> T;
-    const int64_t cols = (a.w.d + 16 * T::kTiles - 1) / (16 * T::kTiles);
-    const int64_t most = (((int64_t)1 << 30) / cols) & ~7;   // row tiles of one launch
-    for (int64_t t = 0; t * T::kRows < a.n_rows; t += most) {
-        const int64_t r = t * T::kRows;
-        MxLinearArgs b = a;
-        b.n_rows = a.n_rows - r < most * T::kRows ? a.n_rows - r : most * T::kRows;
-        b.q = a.q + r * a.ldq;
-        b.s = a.s + r * a.lds;
-        b.y = static_cast<char *>(a.y) + r * a.ldy * (DT == DT_F32 ? 4 : 2);
-        const int64_t rows = (b.n_rows + T::kRows - 1) / T::kRows;
+    by_row_slabs<DT>(a, T::kRows, T::kTiles, [&](const MxLinearArgs &b, int rows, int cols) {
         mx_linear_tile_kernel<DT, FMT, RW, MT, FW, NT, KW>
-            <<<dim3((uint32_t)(rows * cols)), 64 * T::kSet * KW, 0, s>>>(b, (int)rows, (int)cols);
-    }
+            <<<dim3((uint32_t)rows * cols), 64 * T::kSet * KW, 0, s>>>(b, rows, cols);
+    });
 }
 
+// The smallest tile that gives every CU at most one workgroup: fewer, larger
+// workgroups leave CUs idle, more of them repeat reads (us, 1024 wavefronts'
+// worth of k splits on either side; e4m3 on 256 CUs):
+//   24 x 4096 x 4096     16x16 (512 workgroups) 7.2    16x32 (256)  5.6   16x64 (128)  6.1
+//   64 x 4096 x 4096     16x32 (512)            8.1    16x64 (256)  6.6   64x64  (64) 10.0
+//   96 x 4096 x 4096     16x64 (384)           11.2    32x64 (192)  8.2   64x64 (128) 10.1
+//   128 x 4096 x 6144    32x64 (384)           15.2    64x64 (192) 10.6   64x128 (96) 13.9
+//   512 x 14336 x 4096   64x64 (512)           57      64x128 (256) 44    128x256 (64) 147
+// (up to 16 rows twice as many: larger tiles only add features there;
+//   8 x 4096 x 28672     16x64 (448)           12.2    64x128 (224) 15.3).
+// Beyond one round, 64x128 with k in one piece, four workgroups a CU, until the
+// largest tile's rounds (two workgroups a CU in 8 bits, one in 4 bits) are well
+// filled (a CU left with one of two runs it in 4/7 of the pair's time):
+//   1024 x 4096 x 6144   64x128 39.0   128x256 (192 workgroups) 47.6
+//   20000 x 1024 x 1024  64x128 35.7   128x256 (628)            38.8
+//   4096 x 4096 x 6144   64x128 134    128x256 (768)            126
+//   35422 x 4096 x 6144  64x128 1169   128x256 (6672)           1035
+// and in 4 bits
+//   35422 x 512 x 512    64x128 20.5   256x256 (278) 27.3
+//   2048 x 4096 x 6144   64x128 43.2   256x256 (192) 38.0
+//   2048 x 4096 x 4096   64x128 33.9   256x256 (128) 36.2   128x128 (512) 28.7
 template <int DT, int FMT> void linear_pick(const MxLinearArgs &a, hipStream_t s)
 {
-    const uint32_t tiles = (uint32_t)((a.w.d + 31) / 32 * 2);   // both of a pair
-    if (a.n_rows <= 16)
-        mx_linear_few_kernel<DT, FMT, 1, 8><<<dim3(tiles, 1), 512, 0, s>>>(a);
-    else if (a.n_rows <= 32)
-        mx_linear_few_kernel<DT, FMT, 2, 8><<<dim3(tiles, 1), 512, 0, s>>>(a);
-    else if ((a.n_rows + 127) / 128 * ((a.w.d + 255) / 256) >= a.n_cu)
-        linear_tiles<DT, FMT, 2, 4, 2, 8, 1>(a, s);
-    else if ((a.n_rows + 127) / 128 * ((a.w.d + 127) / 128) >= a.n_cu)
-        linear_tiles<DT, FMT, 2, 4, 2, 4, 2>(a, s);
-    else
-        linear_tiles<DT, FMT, 2, 2, 2, 2, 4>(a, s);
+    const int64_t cu = a.n_cu;
+    auto grid = [&](int rows, int features) {
+        return (a.n_rows + rows - 1) / rows * ((a.w.d + features - 1) / features);
+    };
+    const int64_t few = a.n_rows <= 16 ? 2 * cu : cu;
+    if (grid(16, 16) <= few)
+        return linear_direct<DT, FMT, 1, 1>(a, s);
+    if (grid(16, 32) <= few)
+        return linear_direct<DT, FMT, 1, 2>(a, s);
+    if (grid(16, 64) <= few)
+        return linear_direct<DT, FMT, 1, 4>(a, s);
+    if (grid(32, 64) <= cu)
+        return linear_direct<DT, FMT, 2, 4>(a, s);
+    if (grid(64, 64) <= cu)
+        return linear_tiles<DT, FMT, 4, 1, 1, 4, 4>(a, s);
+    if constexpr (FMT == LORA_MX_E4M3) {
+        if (grid(64, 128) <= cu)
+            return linear_tiles<DT, FMT, 4, 1, 1, 8, 4>(a, s);
+        const int64_t n = grid(128, 256), rounds = n / (2 * cu), left = n % (2 * cu);
+        const int64_t sevenths = 7 * rounds + (left > cu ? 7 : left > 0 ? 4 : 0);
+        if (rounds > 0 && n * 7 * 100 >= sevenths * 2 * cu * 82)
+            return linear_tiles<DT, FMT, 2, 4, 2, 8, 1>(a, s);
+    } else {
+        if (grid(64, 128) <= cu)   // two chunks a stage: four sets' slots would not fit LDS
+            return linear_tiles<DT, FMT, 4, 1, 1, 8, 2>(a, s);
+        const int64_t n = grid(256, 256);
+        if (n * 100 >= (n + cu - 1) / cu * cu * 70)
+            return linear_tiles<DT, FMT, 4, 4, 2, 8, 1>(a, s);
+        if (grid(128, 128) >= 2 * cu)
+            return linear_tiles<DT, FMT, 8, 1, 1, 8, 1>(a, s);
+    }
+    linear_tiles<DT, FMT, 4, 1, 1, 8, 1>(a, s);
 }
 
 }  // namespace

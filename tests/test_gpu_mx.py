@@ -263,6 +263,18 @@ def test_linear_whole_numbers(rows, k, d, fmt):
         lb.lora_mx_weight_destroy(h)
 
 
+# One size for every tile that the launcher chooses between (256 CUs): rows and features that end inside a tile,
+# k that ends inside a chunk, a stage of two chunks and a run of four, more wavefront sets than runs of four.
+LINEAR_TILES = [(7, 264, 16000), (24, 1416, 4096), (33, 2312, 4000), (70, 904, 5000), (256, 1416, 4000), (250, 136, 4096),
+                (500, 2312, 4040), (1000, 904, 4600), (4000, 392, 2112), (8190, 648, 4088)]
+
+
+@pytest.mark.parametrize("fmt", (R.E4M3, R.E2M1))
+@pytest.mark.parametrize("rows,k,d", LINEAR_TILES)
+def test_linear_whole_numbers_every_tile(rows, k, d, fmt):
+    test_linear_whole_numbers(rows, k, d, fmt)
+
+
 @pytest.mark.parametrize("fmt", (R.E4M3, R.E2M1))
 @pytest.mark.parametrize("dt", (BF, F32))
 @pytest.mark.parametrize("rows,k,d", [(1, 4096, 512), (16, 14336, 264), (60, 8192, 264), (250, 4104, 512), (600, 2056, 776)])
