@@ -84,9 +84,12 @@ hipError_t launch_rmsnorm_mx(int dtype, const MxNormArgs &a, hipStream_t s);
 // neighbouring features of a row.  The scales of four chunks are 256
 // bytes: byte j of lane l's word is the scale of that lane's block in chunk j.
 // Both are padded with zeros: features to kMxPadRows, scales to four chunks.
+// All tiles of a chunk lie together, so that workgroups at the same k read
+// neighbouring addresses (64 x 4096 x 28672 in 4 bits 13.8 us; with all chunks
+// of a tile together, a power of two apart, 14.5 us).
 struct MxImage {
-    uint8_t *codes;      // [tiles][chunks][64][16]
-    uint8_t *scales;     // [tiles][chunks / 4, rounded up][64][4]
+    uint8_t *codes;      // [chunks][tiles][64][16]
+    uint8_t *scales;     // [chunks / 4, rounded up][tiles][64][4]
     int64_t d;
     int64_t k;
     int tiles;

@@ -142,8 +142,8 @@ __global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        wc[n] = a.w.codes + ((tile0 + n) * chunks * 64 + lane) * 16;
-    const uint8_t *ws = a.w.scales + (tile0 * groups * 64 + lane) * 4;
+        wc[n] = a.w.codes + ((tile0 + n) * 64 + lane) * 16;
+    const uint8_t *ws = a.w.scales + (tile0 * 64 + lane) * 4;
 
     MxChunk<FMT, MT, NT> ring[4];
     u32x4_t sx[MT], sxn[MT];
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(
         const int64_t c = min(4 * grp + j, chunks - 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            ring[j].w[n] = *reinterpret_cast<const u32x4_t *>(wc[n] + c * 1024);
+            ring[j].w[n] = *reinterpret_cast<const u32x4_t *>(wc[n] + c * ((int64_t)a.w.tiles * 1024));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             ring[j].x[t][0] = *reinterpret_cast<const u32x4_t *>(xq[t] + c * (FMT == LORA_MX_E4M3 ? 128 : 64));
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(
             sxn[t] = *reinterpret_cast<const u32x4_t *>(xs[t] + (int64_t)grp * 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            swn[n] = *reinterpret_cast<const uint32_t *>(ws + ((int64_t)n * groups + grp) * 256);
+            swn[n] = *reinterpret_cast<const uint32_t *>(ws + ((int64_t)grp * a.w.tiles + n) * 256);
     };
     auto take_scales = [&]() {
 #pragma unroll
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         xunit[i] = (lane & 7) ^ ((r >> 1) & 7);
         xsrc[i] = a.q + row * a.ldq;
     }
-    const uint8_t *wsrc = a.w.codes + tile0 * chunks * 1024 + lane * 16;
+    const uint8_t *wsrc = a.w.codes + tile0 * 1024 + lane * 16;
     // a set's copies of scales are dealt out to its wavefronts
     constexpr int kDeal = (T::kScaleCopies + T::kSet - 1) / T::kSet;
     const uint8_t *ssrc[kDeal];
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         const int n = i * T::kSet + wv;   // X: a row a lane; W: four tiles of 16 lanes
         const int64_t row = min(row0 + 64 * n + lane, a.n_rows - 1);
         const int64_t tile = tile0 + 4 * (n - T::kXScaleCopies) + (lane >> 4);
-        ssrc[i] = n < T::kXScaleCopies ? a.s + row * a.lds : a.w.scales + tile * groups * 256 + (lane & 15) * 16;
+        ssrc[i] = n < T::kXScaleCopies ? a.s + row * a.lds : a.w.scales + tile * 256 + (lane & 15) * 16;
     }
 
     u32x4_t sx[MT];
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
 #pragma unroll
         for (int i = 0; i < T::kWCopies; ++i) {
             const int b = i * T::kSet + wv, h = b / T::kTiles, tile = b % T::kTiles;
-            mx_copy16(wsrc + ((int64_t)tile * chunks + min(c + h, chunks - 1)) * 1024,
+            mx_copy16(wsrc + ((int64_t)min(c + h, chunks - 1) * a.w.tiles + tile) * 1024,
                       wd + set * T::kWUnits + b * 64);
         }
     };
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         for (int i = 0; i < kDeal; ++i) {
             const int n = i * T::kSet + wv;
             if (n < T::kScaleCopies)
-                mx_copy16(ssrc[i] + (int64_t)grp * (n < T::kXScaleCopies ? 16 : 256),
+                mx_copy16(ssrc[i] + (int64_t)grp * (n < T::kXScaleCopies ? 16 : (int64_t)a.w.tiles * 256),
                           scales + (set * T::kScaleCopies + n) * 64);
         }
     };
@@ -418,7 +418,8 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
             if (t + 1 < MT)
                 read_x(t + 1, h, xd);
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_setprio(1);
+            if constexpr (FMT == LORA_MX_E4M3)
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[t][n] = mx_mfma<FMT, j>(w[n], sw[n], x.v, s, acc[t][n]);

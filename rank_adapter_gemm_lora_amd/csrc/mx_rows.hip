@@ -181,10 +181,10 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_dense_kernel(const void 
     const uint32_t sb = mx_block_scale<LORA_MX_E2M1>(f);
     const int chunk = unit >> 4, lane = 16 * ((unit >> 2) & 3) + mx_image_row(o);
     const int64_t tile = mx_image_tile(o);
-    *reinterpret_cast<uint32_t *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16 +
+    *reinterpret_cast<uint32_t *>(w.codes + (((int64_t)chunk * w.tiles + tile) * 64 + lane) * 16 +
                                   4 * (unit & 3)) = mx_codes<LORA_MX_E2M1>(f, sb);
     if ((unit & 3) == 0) {
-        uint8_t *sc = w.scales + ((tile * groups + (chunk >> 2)) * 64 + lane) * 4;
+        uint8_t *sc = w.scales + (((int64_t)(chunk >> 2) * w.tiles + tile) * 64 + lane) * 4;
         sc[chunk & 3] = (uint8_t)sb;
         if (chunk == w.chunks - 1)
             for (int j = w.chunks; j < groups * 4; ++j)
@@ -213,8 +213,8 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b
     }
     const int chunk = blk >> 2, lane = 16 * (blk & 3) + mx_image_row(o);
     const int64_t tile = mx_image_tile(o);
-    *reinterpret_cast<uint4 *>(w.codes + ((tile * w.chunks + chunk) * 64 + lane) * 16) = c;
-    uint8_t *sc = w.scales + ((tile * groups + (chunk >> 2)) * 64 + lane) * 4;
+    *reinterpret_cast<uint4 *>(w.codes + (((int64_t)chunk * w.tiles + tile) * 64 + lane) * 16) = c;
+    uint8_t *sc = w.scales + (((int64_t)(chunk >> 2) * w.tiles + tile) * 64 + lane) * 4;
     sc[chunk & 3] = (uint8_t)sb;
     if (chunk == w.chunks - 1)
         for (int j = w.chunks; j < groups * 4; ++j)
