@@ -64,7 +64,8 @@ struct MxNormArgs {
     const void *res;     // or null
     int64_t ldr;
     const void *weight;
-    float eps;
+    double eps;
+    double inv_k;        // 1 / k
     void *h;             // or null
     int64_t ldh;
     void *out;           // or null

@@ -222,6 +222,7 @@ lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *
     a.ldr = ldr;
     a.weight = weight;
     a.eps = eps;
+    a.inv_k = 1. / (double)k;
     a.h = h_out;
     a.ldh = ldh;
     a.out = out;

@@ -54,8 +54,10 @@ __global__ __launch_bounds__(kRowThreads) void mx_quantize_kernel(MxRowArgs a)
 
 // g / (1 + exp(-g)) * u.  exp(-g) = 2^t (1 + r ln 2) with t = -g log2(e) rounded
 // and r what the rounding and log2(e)'s own lost (its low part), so that the
-// error does not grow with |g|; 2^t and the reciprocal are the hardware's, within
-// 2^-23 of their values: under 8 roundings of 2^-24 in all.  The reciprocal of
+// error does not grow with |g|; 2^t is the hardware's, within 2^-23 of its
+// value.  The quotient is g times the hardware's reciprocal and one correction
+// by what is left of g: 4.5e-8 of the values in the root mean square, as with
+// expf and a division (4.8e-8 without it, in the same time).  The reciprocal of
 // a denominator past 2^126 would be flushed, so past 2^64 it is taken of a
 // scaled one.
 __device__ __forceinline__ float mx_silu_mul(float g, float u)
@@ -64,9 +66,11 @@ __device__ __forceinline__ float mx_silu_mul(float g, float u)
     const float t = -g * kLog2e;
     const float r = fmaf(-g, kLog2e, -t) - g * kLog2eLow;
     const float e = __builtin_amdgcn_exp2f(t);
-    const float d = 1.f + (e < INFINITY ? fmaf(e, r * kLn2, e) : e);
+    const float d = 1.f + (e > 0.f && e < INFINITY ? fmaf(e, r * kLn2, e) : e);   // r may be NaN else
     const float k = d > 0x1p64f ? 0x1p-64f : 1.f;
-    return g * __builtin_amdgcn_rcpf(d * k) * k * u;
+    const float rc = __builtin_amdgcn_rcpf(d * k), q = g * rc;
+    const float left = fmaf(-(d * k), q, g);   // NaN where g or d is not finite: q stands
+    return (left == left ? fmaf(left, rc, q) : q) * k * u;
 }
 
 // silu(g) * u -> a dense row and blocks (512 x 14336 bf16: 12.7 us, 51 MB at 4
@@ -221,13 +225,33 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b
             sc[j & 3] = 0;
 }
 
+// 1 / sqrt(m) as a sum x + y: the hardware's reciprocal root (within 2^-23; small
+// m scaled, it would be flushed), one Newton step on m's high and low parts, and
+// what rounding that step loses.  y is 0 where m is 0 or not finite.
+__device__ __forceinline__ float2 mx_inv_sqrt(double m)
+{
+    const bool tiny = m < 0x1p-96;
+    m *= tiny ? 0x1p64 : 1.;
+    const float hi = (float)m, lo = (float)(m - hi);
+    const float r = __builtin_amdgcn_rsqf(hi);
+    float x = r, y = 0.f;
+    if (hi > 0.f && hi < INFINITY) {
+        const float t = hi * r, tl = fmaf(hi, r, -t);
+        const float left = fmaf(-t, r, 1.f) - fmaf(lo * r, r, tl * r);   // 1 - m r^2
+        x = fmaf(0.5f * r, left, r);
+        y = fmaf(0.5f * r, left, -(x - r));
+    }
+    const float k = tiny ? 0x1p32f : 1.f;
+    return make_float2(x * k, y * k);
+}
+
 // One row per workgroup of T threads; the row stays in registers, NU units of 8
 // a thread (unit t + T j), so x and the residual are read once and nothing is
 // written before the whole row is in.
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
 {
-    __shared__ float part[T / 64];
+    __shared__ double part[T / 64];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const int units = (int)((a.k + kMxChunk - 1) / kMxChunk) * (kMxChunk / 8);
@@ -244,17 +268,18 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
         }
     }
     float f[NU][8];
-    float sum = 0.f;
+    double sum = 0.;   // of each unit's fp32 sum
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-        float r[8];
+        float r[8], part8 = 0.f;
         vx[j].to_f32(f[j]);
         vr[j].to_f32(r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f[j][e] += r[e];
-            sum = fmaf(f[j][e], f[j][e], sum);
+            part8 = fmaf(f[j][e], f[j][e], part8);
         }
+        sum += part8;
     }
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1)
@@ -263,12 +288,12 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
         if ((tid & 63) == 0)
             part[tid >> 6] = sum;
         __syncthreads();
-        sum = 0.f;
+        sum = 0.;
 #pragma unroll
         for (int w = 0; w < T / 64; ++w)
             sum += part[w];
     }
-    const float inv = 1.f / sqrtf(sum / (float)a.k + a.eps);
+    const float2 inv = mx_inv_sqrt(sum * a.inv_k + a.eps);
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
         const int unit = tid + T * j;
@@ -281,8 +306,14 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
             float w[8];
             vw.to_f32(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[j][e] = f[j][e] * inv * w[e];
+            for (int e = 0; e < 8; ++e) {
+                // h inv w with what its first product loses, so that n is near
+                // the once-rounded value: its codes depend on which side of a
+                // border it falls.  (p not finite: the lost part is not used.)
+                const float p = f[j][e] * inv.x;
+                const float l = fmaf(f[j][e], inv.x, -p) + f[j][e] * inv.y;
+                f[j][e] = fabsf(p) < INFINITY ? fmaf(p, w[e], l * w[e]) : p * w[e];
+            }
             if (a.out)
                 Vec8<DT>::store(a.out, row * a.ldo + c, f[j]);
         }

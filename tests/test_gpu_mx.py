@@ -431,3 +431,44 @@ def test_far_offsets():
         np.testing.assert_array_equal(y, near)
     finally:
         lb.lora_mx_weight_destroy(h)
+
+
+def test_swiglu_far_and_infinite_gates():
+    """Gates where exp overflows or vanishes, infinities and NaN: the formula's value in fp32's range."""
+    gates = [0.0, -0.0, 1e-30, -1e-30, 60.0, -60.0, 87.0, -87.0, -88.5, -100.0, 200.0, 1e30, -1e30, np.inf, -np.inf, np.nan]
+    ups = [1.0, -2.5, 1e30, 1e-30]
+    n, f = len(ups), len(gates)
+    x, hx = dense(np.concatenate([np.tile(gates, (n, 1)), np.repeat(np.array(ups)[:, None], f, 1)], 1), F32)
+    out = torch.empty(n, f, dtype=torch.float32, device=DEV)
+    note("swiglu far gates")
+    lb.lora_swiglu_mx(out.data_ptr(), f, 0, 0, 0, 0, x.data_ptr(), 2 * f, F32, n, f, stream())
+    got = out.double().cpu().numpy()
+    g, u = hx[:, :f], hx[:, f:]
+    with np.errstate(all="ignore"):
+        ex = g / (1 + np.exp(-g)) * u
+        ex = np.where(np.abs(ex) > np.finfo(np.float32).max, np.copysign(np.inf, ex), ex)
+        far = (g < -88.73) & np.isfinite(g)   # fp32's exp(-g) overflows past 88.73, and the quotient is 0
+        # 16 u of the value, and one subnormal step of each of the two products under 2^-126
+        ok = np.abs(got - ex) <= 16 * 2.0 ** -24 * np.abs(ex) + 2.0 ** -149 * (1 + np.abs(u))
+    ok |= (got == ex) | (np.isnan(got) & np.isnan(ex))
+    ok[far] = got[far] == 0
+    assert ok.all(), np.argwhere(~ok).tolist()
+
+
+def test_rmsnorm_tiny_and_huge_rows():
+    """Rows whose mean square is far from one: the root's scaling, and squares past the range (infinite mean: zeros)."""
+    rows, k = 4, 256
+    g = np.random.default_rng(11)
+    v = g.standard_normal((rows, k)) * np.array([1e-16, 1e-18, 1e15, 1e25])[:, None]
+    x, hx = dense(v, F32)
+    w, hw = dense(np.ones((1, k)), F32)
+    out = torch.empty_like(x)
+    note("rmsnorm tiny and huge rows")
+    lb.lora_rmsnorm_mx(out.data_ptr(), k, 0, 0, 0, 0, 0, 0, x.data_ptr(), k, 0, 0, w.data_ptr(), 0.0, F32, rows, k, stream())
+    got = out.double().cpu().numpy()
+    _, en = R.norm(hx, None, hw, 0.0)
+    # squares of 1e-18 and below round to 2^-149: half of that on each of k / 2 or more terms of mean 1e-36
+    check_dense(got[:1], en[:1], F32, 2.0 ** -18, "tiny")
+    check_dense(got[1:2], en[1:2], F32, 2.0 ** -12, "tinier")
+    check_dense(got[2:3], en[2:3], F32, 2.0 ** -18, "huge")
+    assert (got[3] == 0).all()
