@@ -476,8 +476,9 @@ lora_status lora_mx_weight_load_packed(lora_mx_weight *w, const void *q, int64_t
 /*
  * y = X W^T: y[i][o] = round(sum_b 2^(es + ew) sum_{j in b} X[i][j] W[o][j])
  * over the blocks b of k, for every row i and o < d; X in blocks (q, s) of
- * either format, products and sums in fp32 on the matrix cores, one rounding
- * to dtype.  y [n_rows][ldy] is written, columns >= d are not touched.  A NaN
+ * either format.  Products and the sums of each eight neighbouring ones are
+ * exact, those meet in fp32 on the matrix cores, and y is rounded once to
+ * dtype.  y [n_rows][ldy] is written, columns >= d are not touched.  A NaN
  * scale or element makes its row (of X) or column (of W) NaN.  The order of
  * the sums depends on the shapes alone.  Errors: LORA_E_ARG, LORA_E_EMPTY
  * (nothing was loaded into w), LORA_E_UNSUPPORTED, LORA_E_HIP.
