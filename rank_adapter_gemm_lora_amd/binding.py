@@ -293,14 +293,16 @@ def lora_mx_scale_bytes(k: int) -> int:
 
 def lora_mx_quantize(q: int, ldq: int, s: int, lds: int, fmt: int, x: int, ldx: int, dtype: int,
                      n_rows: int, k: int, stream=None):
-    _check(load().lora_mx_quantize(q, ldq, s, lds, fmt, x, ldx, dtype, n_rows, k, stream),
-           "lora_mx_quantize")
+    st = (_lib or load()).lora_mx_quantize(q, ldq, s, lds, fmt, x, ldx, dtype, n_rows, k, stream)
+    if st:
+        _check(st, "lora_mx_quantize")
 
 
 def lora_mx_dequantize(x: int, ldx: int, dtype: int, q: int, ldq: int, s: int, lds: int, fmt: int,
                        n_rows: int, k: int, stream=None):
-    _check(load().lora_mx_dequantize(x, ldx, dtype, q, ldq, s, lds, fmt, n_rows, k, stream),
-           "lora_mx_dequantize")
+    st = (_lib or load()).lora_mx_dequantize(x, ldx, dtype, q, ldq, s, lds, fmt, n_rows, k, stream)
+    if st:
+        _check(st, "lora_mx_dequantize")
 
 
 def lora_mx_weight_create(d: int, k: int):
@@ -325,23 +327,26 @@ def lora_mx_weight_load_packed(w, q: int, ldq: int, s: int, lds: int, stream=Non
 
 def lora_mx_linear(w, y: int, ldy: int, dtype: int, q: int, ldq: int, s: int, lds: int, fmt: int,
                    n_rows: int, stream=None):
-    _check(load().lora_mx_linear(w, y, ldy, dtype, q, ldq, s, lds, fmt, n_rows, stream),
-           "lora_mx_linear")
+    st = (_lib or load()).lora_mx_linear(w, y, ldy, dtype, q, ldq, s, lds, fmt, n_rows, stream)
+    if st:
+        _check(st, "lora_mx_linear")
 
 
 def lora_rmsnorm_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, h_out: int, ldh: int,
                     x: int, ldx: int, residual: int, ldr: int, weight: int, eps: float, dtype: int,
                     n_rows: int, k: int, stream=None):
     """Pointers of outputs and of the residual may be 0 (not wanted / none)."""
-    _check(load().lora_rmsnorm_mx(out, ldo, q, ldq, s, lds, h_out, ldh, x, ldx, residual, ldr,
-                                  weight, eps, dtype, n_rows, k, stream), "lora_rmsnorm_mx")
+    st = (_lib or load()).lora_rmsnorm_mx(out, ldo, q, ldq, s, lds, h_out, ldh, x, ldx, residual, ldr, weight, eps, dtype, n_rows, k, stream)
+    if st:
+        _check(st, "lora_rmsnorm_mx")
 
 
 def lora_swiglu_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, gu: int, ldg: int,
                    dtype: int, n_rows: int, f: int, stream=None):
     """out, or q with s, may be 0 (not wanted)."""
-    _check(load().lora_swiglu_mx(out, ldo, q, ldq, s, lds, gu, ldg, dtype, n_rows, f, stream),
-           "lora_swiglu_mx")
+    st = (_lib or load()).lora_swiglu_mx(out, ldo, q, ldq, s, lds, gu, ldg, dtype, n_rows, f, stream)
+    if st:
+        _check(st, "lora_swiglu_mx")
 
 
 def lora_residency_create(stack, max_cpu_adapters: int, n_slots: int = 0, r_max: int = 0,
