@@ -92,6 +92,31 @@ __device__ __forceinline__ void mx_store8(void *y, int64_t idx, f32x4_t u, f32x4
     Vec8<DT>::store(y, idx, f);
 }
 
+// Row and column tile of a workgroup.  Workgroups of one XCD walk bands of eight
+// row tiles, so that its L2 serves the X rows and W tiles that they share; the
+// divisions' multipliers come from the host.
+struct MxGrid {
+    int rows, cols;
+    MxDiv band;   // by 8 cols
+    MxDiv last;   // by the last band's row tiles, where they are fewer than eight
+};
+inline MxGrid mx_grid(int rows, int cols)
+{
+    return MxGrid{rows, cols, mx_div(8u * cols), mx_div(rows % 8 ? rows % 8 : 8)};
+}
+struct MxPlace {
+    int row, col;
+};
+__device__ __forceinline__ MxPlace mx_place(const MxGrid &g)
+{
+    const uint32_t id = (uint32_t)xcd_major(blockIdx.x, gridDim.x);
+    const uint32_t band = mx_div_of(id, g.band), in = id - band * g.band.d;
+    if ((int)band * 8 + 8 <= g.rows)
+        return MxPlace{(int)(band * 8 + (in & 7)), (int)(in >> 3)};
+    const uint32_t col = mx_div_of(in, g.last);
+    return MxPlace{(int)(band * 8 + in - col * g.last.d), (int)col};
+}
+
 template <class F, int... I> __device__ __forceinline__ void mx_for(F f, std::integer_sequence<int, I...>)
 {
     (f(std::integral_constant<int, I>{}), ...);
@@ -118,24 +143,22 @@ template <int FMT, int MT, int NT> struct MxChunk {
 };
 
 template <int DT, int FMT, int MT, int NT>
-__global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(MxLinearArgs a, int row_tiles, int col_tiles)
+__global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(MxLinearArgs a, MxGrid grid)
 {
     constexpr int NW = kDirectWaves;
     constexpr int kPair = NT > 1 ? 2 : 1, kParts = MT * NT / kPair;
     __shared__ f32x4_t part[NW][MT * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const int id = xcd_major(blockIdx.x, gridDim.x);
-    const int band = id / (8 * col_tiles), in = id % (8 * col_tiles);
-    const int tall = min(8, row_tiles - 8 * band);
-    const int64_t row0 = (int64_t)(8 * band + in % tall) * (16 * MT);
-    const int64_t tile0 = (int64_t)(in / tall) * NT;
+    const MxPlace at = mx_place(grid);
+    const int n_rows = (int)a.n_rows, row0 = at.row * (16 * MT);
+    const int64_t tile0 = (int64_t)at.col * NT;
     const int chunks = a.w.chunks, groups = (chunks + 3) / 4;
     const uint8_t *xq[MT], *xs[MT], *wc[NT];
     f32x4_t acc[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t r = min(row0 + 16 * t + m, a.n_rows - 1);   // rows past the end repeat the last one
+        const uint32_t r = min(row0 + 16 * t + m, n_rows - 1);   // rows past the end repeat the last one
         xq[t] = a.q + r * a.ldq + 16 * g;
         xs[t] = a.s + r * a.lds;
 #pragma unroll
@@ -255,15 +278,15 @@ __global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(
             for (int w = 0; w < NW; ++w)
                 v[i] += w == p % NW ? acc[f / NT][f % NT] : part[w][f][lane];
         }
-        const int64_t r = row0 + 16 * (kPair * p / NT) + m;
+        const int r = row0 + 16 * (kPair * p / NT) + m;
         if constexpr (kPair == 2) {
             const int64_t o = (tile0 + kPair * p % NT) * 16 + 8 * g;
-            if (r < a.n_rows && o < a.w.d)
-                mx_store8<DT>(a.y, r * a.ldy + o, v[0], v[1]);
+            if (r < n_rows && o < a.w.d)
+                mx_store8<DT>(a.y, (int64_t)r * a.ldy + o, v[0], v[1]);
         } else {
             const int64_t o = (tile0 >> 1) * 32 + 8 * g + 4 * (tile0 & 1);
-            if (r < a.n_rows && o < a.w.d)
-                mx_store4<DT>(a.y, r * a.ldy + o, v[0]);
+            if (r < n_rows && o < a.w.d)
+                mx_store4<DT>(a.y, (int64_t)r * a.ldy + o, v[0]);
         }
     }
 }
@@ -319,8 +342,7 @@ __device__ __forceinline__ void mx_copy16(const uint8_t *src, u32x4_t *dst)
 }
 
 template <int DT, int FMT, int RW, int MT, int FW, int NT, int KW>
-__global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(MxLinearArgs a, int row_tiles,
-                                                                              int col_tiles)
+__global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(MxLinearArgs a, MxGrid grid)
 {
     typedef MxTile<DT, FMT, RW, MT, FW, NT, KW> T;
     __shared__ u32x4_t x0[KW * T::kXUnits], x1[KW * T::kXUnits];
@@ -331,13 +353,9 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     const int set = wave / T::kSet, wv = wave % T::kSet;
     const int wr = wv / FW, wf = wv % FW;
     const int g = lane >> 4, m = lane & 15;
-    // workgroups of one XCD walk bands of eight row tiles, so that its L2 serves
-    // the X rows and W tiles that they share
-    const int id = xcd_major(blockIdx.x, gridDim.x);
-    const int band = id / (8 * col_tiles), in = id % (8 * col_tiles);
-    const int tall = min(8, row_tiles - 8 * band);
-    const int64_t row0 = (int64_t)(8 * band + in % tall) * T::kRows;
-    const int64_t tile0 = (int64_t)(in / tall) * T::kTiles;
+    const MxPlace at = mx_place(grid);
+    const int n_rows = (int)a.n_rows, row0 = at.row * T::kRows;
+    const int64_t tile0 = (int64_t)at.col * T::kTiles;
     const int chunks = a.w.chunks, groups = (chunks + 3) / 4;
     // this set's groups of four chunks
     const int per = (groups + KW - 1) / KW;
@@ -348,7 +366,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
 #pragma unroll
     for (int i = 0; i < T::kXCopies; ++i) {
         const int r = (i * T::kSet + wv) * 8 + (lane >> 3);
-        const int64_t row = min(row0 + r, a.n_rows - 1);   // rows past the end repeat the last one
+        const uint32_t row = min(row0 + r, n_rows - 1);   // rows past the end repeat the last one
         xunit[i] = (lane & 7) ^ ((r >> 1) & 7);
         xsrc[i] = a.q + row * a.ldq;
     }
@@ -359,7 +377,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
 #pragma unroll
     for (int i = 0; i < kDeal; ++i) {
         const int n = i * T::kSet + wv;   // X: a row a lane; W: four tiles of 16 lanes
-        const int64_t row = min(row0 + 64 * n + lane, a.n_rows - 1);
+        const uint32_t row = min(row0 + 64 * n + lane, n_rows - 1);
         const int64_t tile = tile0 + 4 * (n - T::kXScaleCopies) + (lane >> 4);
         ssrc[i] = n < T::kXScaleCopies ? a.s + row * a.lds : a.w.scales + tile * 256 + (lane & 15) * 16;
     }
@@ -535,12 +553,12 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t r = row0 + 16 * (wr * MT + t) + m;
+        const int r = row0 + 16 * (wr * MT + t) + m;
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
             const int64_t o = (tile0 + wf * NT + n) * 16 + 8 * g;
-            if (r < a.n_rows && o < a.w.d)
-                mx_store8<DT>(a.y, r * a.ldy + o, acc[t][n], acc[t][n + 1]);
+            if (r < n_rows && o < a.w.d)
+                mx_store8<DT>(a.y, (int64_t)r * a.ldy + o, acc[t][n], acc[t][n + 1]);
         }
     }
 }
@@ -566,7 +584,7 @@ template <int DT, int FMT, int MT, int NT> void linear_direct(const MxLinearArgs
     constexpr int kPer = NT == 1 ? 2 : 1;
     by_row_slabs<DT>(a, 16 * MT, NT * kPer, [&](const MxLinearArgs &b, int rows, int cols) {
         mx_linear_direct_kernel<DT, FMT, MT, NT>
-            <<<dim3((uint32_t)rows * cols * kPer), 64 * kDirectWaves, 0, s>>>(b, rows, cols * kPer);
+            <<<dim3((uint32_t)rows * cols * kPer), 64 * kDirectWaves, 0, s>>>(b, mx_grid(rows, cols * kPer));
     });
 }
 
@@ -576,7 +594,7 @@ void linear_tiles(const MxLinearArgs &a, hipStream_t s)
     typedef MxTile<DT, FMT, RW, MT, FW, NT, KW> T;
     by_row_slabs<DT>(a, T::kRows, T::kTiles, [&](const MxLinearArgs &b, int rows, int cols) {
         mx_linear_tile_kernel<DT, FMT, RW, MT, FW, NT, KW>
-            <<<dim3((uint32_t)rows * cols), 64 * T::kSet * KW, 0, s>>>(b, rows, cols);
+            <<<dim3((uint32_t)rows * cols), 64 * T::kSet * KW, 0, s>>>(b, mx_grid(rows, cols));
     });
 }
 
