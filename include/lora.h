@@ -414,7 +414,8 @@ lora_status lora_build_apply_plan(const lora_stack *st, int64_t n_rows, const lo
  *
  * Matrices in LORA_F32 or LORA_BF16 follow the conventions at the top (row
  * strides in elements, multiples of 8; k a multiple of 8; 16-byte aligned).
- * n_rows 0 checks its arguments' values and does nothing.  All sums are fp32.
+ * n_rows 0 checks its arguments' values and does nothing.  All sums are fp32
+ * or wider.
  * Nothing is allocated per call, and every call can be captured in a HIP
  * graph.  Limits: k <= 2^20 (lora_rmsnorm_mx: 2^16), d <= 2^22, n_rows <
  * 2^30; beyond them LORA_E_UNSUPPORTED.
@@ -494,7 +495,9 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
  *      n = h * (mean_j h_j^2 + eps)^-1/2 * weight
  *      h_out = round(h),  out = round(n),  (q, s) = n in e4m3 blocks
  *
- * each output rounded once from the fp32 h or n.  weight: DEVICE [k], dtype.
+ * h_out rounded once from the fp32 h, out from the fp32 n; the codes are those of
+ * n before its rounding to fp32 (a value beside the middle of two codes falls on
+ * its own side), and h_j^2 is summed in 64 bits.  weight: DEVICE [k], dtype.
  * out, h_out, and q with s may each be NULL, not all of them.  h_out and out
  * may be x or residual themselves with the same stride (in place); otherwise
  * the outputs overlap nothing.  eps >= 0.  A row whose h_j^2 all vanish and

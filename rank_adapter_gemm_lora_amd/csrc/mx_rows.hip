@@ -56,8 +56,8 @@ __global__ __launch_bounds__(kRowThreads) void mx_quantize_kernel(MxRowArgs a)
 // and r what the rounding and log2(e)'s own lost (its low part), so that the
 // error does not grow with |g|; 2^t is the hardware's, within 2^-23 of its
 // value.  The quotient is g times the hardware's reciprocal and one correction
-// by what is left of g: 4.5e-8 of the values in the root mean square, as with
-// expf and a division (4.8e-8 without it, in the same time).  The reciprocal of
+// by what is left of g: 3.6e-8 - 4.5e-8 of the values in the root mean square, as
+// with expf and a division (4.8e-8 without it, in the same time).  The reciprocal of
 // a denominator past 2^126 would be flushed, so past 2^64 it is taken of a
 // scaled one.
 __device__ __forceinline__ float mx_silu_mul(float g, float u)
@@ -73,8 +73,9 @@ __device__ __forceinline__ float mx_silu_mul(float g, float u)
     return (left == left ? fmaf(left, rc, q) : q) * k * u;
 }
 
-// silu(g) * u -> a dense row and blocks (512 x 14336 bf16: 12.7 us, 51 MB at 4
-// TB/s; 13.4 us with expf and a true division, bound by their instructions).
+// silu(g) * u -> a dense row and blocks (512 x 14336 bf16: 13.3 us, 51 MB at 3.9
+// TB/s; 15.0 us with expf and a true division, bound by their instructions, and
+// the same errors).
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void swiglu_mx_kernel(MxRowArgs a)
 {
@@ -245,9 +246,26 @@ __device__ __forceinline__ float2 mx_inv_sqrt(double m)
     return make_float2(x * k, y * k);
 }
 
+// n + l (l under half a step of n) rounded to odd: towards zero, then the last
+// bit set; n itself if l is 0 or not finite.  Rounding that to a shorter format
+// gives what n + l itself rounds to, which n would not on a border (l decides).
+// l is 0 where n is: the sign's subtraction never passes 0.
+__device__ __forceinline__ float mx_to_odd(float n, float l)
+{
+    constexpr int kFiniteNotZero = 0x198;   // normals and subnormals of either sign
+    const int b = __float_as_int(n);
+    const int odd = (b + ((__float_as_int(l) ^ b) >> 31)) | 1;
+    return __int_as_float(__builtin_amdgcn_classf(l, kFiniteNotZero) ? odd : b);
+}
+
 // One row per workgroup of T threads; the row stays in registers, NU units of 8
 // a thread (unit t + T j), so x and the residual are read once and nothing is
 // written before the whole row is in.
+// The squares are summed in 64 bits, so that the codes of n + lost are the exact
+// value's but for its last bits: none of 4.3 M differed (fp32 sums: 4, and codes
+// of the rounded n: 7).  35422 x 4096 bf16: 226 - 232 us, 1.3 GB at 5.7 TB/s,
+// and as long without either; 300 x 14336, one to two rows a CU and bound by
+// their instructions: 16.0 us with its inverse, 14.9 without.
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
 {
@@ -268,18 +286,17 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
         }
     }
     float f[NU][8];
-    double sum = 0.;   // of each unit's fp32 sum
+    double sum = 0.;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-        float r[8], part8 = 0.f;
+        float r[8];
         vx[j].to_f32(f[j]);
         vr[j].to_f32(r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f[j][e] += r[e];
-            part8 = fmaf(f[j][e], f[j][e], part8);
+            sum = fma((double)f[j][e], (double)f[j][e], sum);
         }
-        sum += part8;
     }
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1)
@@ -303,19 +320,20 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
                 Vec8<DT>::store(a.h, row * a.ldh + c, f[j]);
             Vec8<DT> vw;
             vw.load(a.weight, c);
-            float w[8];
+            float w[8], n[8];
             vw.to_f32(w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // h inv w with what its first product loses, so that n is near
-                // the once-rounded value: its codes depend on which side of a
-                // border it falls.  (p not finite: the lost part is not used.)
-                const float p = f[j][e] * inv.x;
+                // h inv w and what its roundings lose: n is near the once-rounded
+                // value, and its codes are taken of n + lost, not of n.  (A product
+                // that is not finite stands without the lost part.)
+                const float p = f[j][e] * inv.x, pw = p * w[e];
                 const float l = fmaf(f[j][e], inv.x, -p) + f[j][e] * inv.y;
-                f[j][e] = fabsf(p) < INFINITY ? fmaf(p, w[e], l * w[e]) : p * w[e];
+                n[e] = fabsf(pw) < INFINITY ? fmaf(p, w[e], l * w[e]) : pw;
+                f[j][e] = mx_to_odd(n[e], fmaf(l, w[e], fmaf(p, w[e], -n[e])));
             }
             if (a.out)
-                Vec8<DT>::store(a.out, row * a.ldo + c, f[j]);
+                Vec8<DT>::store(a.out, row * a.ldo + c, n);
         }
         if (a.b.q && unit < units)   // whole 16-lane groups
             mx_store_unit<LORA_MX_E4M3>(a.b.q + row * a.b.ldq, a.b.s + row * a.b.lds, unit, units,

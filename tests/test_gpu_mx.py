@@ -455,6 +455,44 @@ def test_swiglu_far_and_infinite_gates():
     assert ok.all(), np.argwhere(~ok).tolist()
 
 
+def test_rmsnorm_codes_beside_a_border():
+    """Values within 2^-26 of the middle of two codes: fp32's nearest is the middle itself, the codes still fall right.
+
+    h is near 2^-30, so mean h^2 + 1 is 1 in 64 bits and n = h w.  With a = 2^-9, (1 + a)(1 - a + a^2) = 1 + 2^-27, and with
+    b = 2^-13, (1 + b)(1 - b) = 1 - 2^-26.  The middles are odd sixteenths; every factor has at most 23 bits.
+    """
+    a, b, k = 2.0 ** -9, 2.0 ** -13, 264
+    pairs = [(2.0 ** -30 * up * sign, m / 16 * rest) for m in (17, 19, 21, 23, 25, 27) for sign in (1, -1)
+             for up, rest in ((1 + a, 1 - a + a * a), (1 + b, 1 - b))]
+    hv, wv = np.resize(np.array(pairs), (k, 2)).T
+    x, hx = dense(hv[None], F32)
+    w, hw = dense(wv[None], F32)
+    assert (hx == hv).all() and (hw == wv).all()
+    exact = hx * hw   # at most 46 bits
+    middle = exact.astype(np.float32).astype(np.float64)
+    assert (np.abs(middle) * 2.0 ** 34 % 2 == 1).all() and (middle != exact).all()
+    q, s = blocks(1, k, R.E4M3)
+    note("rmsnorm beside a border")
+    lb.lora_rmsnorm_mx(0, 0, *held(q, s), 0, 0, x.data_ptr(), k, 0, 0, w.data_ptr(), 1.0, F32, 1, k, stream())
+    check_blocks(q.cpu().numpy(), s.cpu().numpy(), exact, 0.0, k)
+
+
+def test_rmsnorm_weights_not_finite():
+    """h inv w with an infinite or NaN weight: the product's value, and blocks of NaN around it."""
+    k = 264
+    x, hx = dense(np.where(np.arange(k) % 2, 1.0, -1.0)[None], F32)   # inv is 1
+    wv = np.ones((1, k))
+    wv[0, [0, 1, 40, 77]] = np.inf, np.inf, -np.inf, np.nan
+    w, hw = dense(wv, F32)
+    out = torch.empty_like(x)
+    q, s = blocks(1, k, R.E4M3)
+    note("rmsnorm weights not finite")
+    lb.lora_rmsnorm_mx(out.data_ptr(), k, *held(q, s), 0, 0, x.data_ptr(), k, 0, 0, w.data_ptr(), 0.0, F32, 1, k, stream())
+    np.testing.assert_array_equal(out.double().cpu().numpy(), hx * hw)
+    gs = s.cpu().numpy()[0, :9]
+    assert (gs[:3] == 255).all() and (gs[3:] == 127 - 8).all()
+
+
 def test_rmsnorm_tiny_and_huge_rows():
     """Rows whose mean square is far from one: the root's scaling, and squares past the range (infinite mean: zeros)."""
     rows, k = 4, 256
