@@ -455,6 +455,21 @@ def test_swiglu_far_and_infinite_gates():
     assert ok.all(), np.argwhere(~ok).tolist()
 
 
+@pytest.mark.parametrize("dt", (BF, F32))
+def test_swiglu_is_near_the_operations_one_by_one(dt):
+    """Against fp32 operations in turn: under one step of fp32, and so (bf16) the same or the neighbouring value."""
+    n, f = 64, 4096
+    x, _ = dense(rand(23, n, 2 * f, 1.0), dt)
+    out = torch.empty(n, f, dtype=TD[dt], device=DEV)
+    note("swiglu against fp32 operations")
+    lb.lora_swiglu_mx(out.data_ptr(), f, 0, 0, 0, 0, x.data_ptr(), 2 * f, dt, n, f, stream())
+    g, u = x[:, :f].float().cpu(), x[:, f:2 * f].float().cpu()
+    want = (g / (1 + torch.exp(-g)) * u).to(TD[dt]).double()
+    got = out.double().cpu()
+    # exp within 2^-23 on either side; sum, quotient and product half a step each on both sides: 2 + 3 steps of 2^-23
+    assert ((got - want).abs() <= (5 * 2.0 ** -23 + (2.0 ** -7 if dt == BF else 0)) * want.abs() + 2.0 ** -126).all()
+
+
 def test_rmsnorm_codes_beside_a_border():
     """Values within 2^-26 of the middle of two codes: fp32's nearest is the middle itself, the codes still fall right.
 
