@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "mx_slabs.h"
 
 namespace lora {
 
@@ -71,6 +72,7 @@ struct MxNormArgs {
     void *out;           // or null
     int64_t ldo;
     MxBlocks b;          // b.q null: not wanted
+    int64_t row0;        // first row of this launch
     int64_t n_rows;
     int64_t k;
 };

@@ -563,28 +563,30 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     }
 }
 
-// Launch `go` over slabs of rows, so that a launch has at most 2^29 tiles.
-template <int DT, class F> void by_row_slabs(const MxLinearArgs &a, int rows, int tiles, F go)
+// Launch `go` over slabs of rows: row tiles of `rows` rows by column tiles of
+// `tiles` times 16 features, `per` workgroups of `threads` each.
+template <int DT, class F>
+void by_row_slabs(const MxLinearArgs &a, int rows, int tiles, int per, int threads, F go)
 {
     const int64_t cols = (a.w.d + 16 * tiles - 1) / (16 * tiles);
-    const int64_t most = ((((int64_t)1 << 29) / cols) & ~(int64_t)7) * rows;
-    for (int64_t r = 0; r < a.n_rows; r += most) {
+    for_slabs(a.n_rows, slab_rows(rows, cols * per, threads), [&](int64_t r, int64_t n) {
         MxLinearArgs b = a;
-        b.n_rows = a.n_rows - r < most ? a.n_rows - r : most;
+        b.n_rows = n;
         b.q = a.q + r * a.ldq;
         b.s = a.s + r * a.lds;
         b.y = static_cast<char *>(a.y) + r * a.ldy * (DT == DT_F32 ? 4 : 2);
-        go(b, (int)((b.n_rows + rows - 1) / rows), (int)cols);
-    }
+        go(b, (int)((n + rows - 1) / rows), (int)cols);
+    });
 }
 
 template <int DT, int FMT, int MT, int NT> void linear_direct(const MxLinearArgs &a, hipStream_t s)
 {
     // one tile a workgroup: both of every pair
     constexpr int kPer = NT == 1 ? 2 : 1;
-    by_row_slabs<DT>(a, 16 * MT, NT * kPer, [&](const MxLinearArgs &b, int rows, int cols) {
+    constexpr int kThreads = 64 * kDirectWaves;
+    by_row_slabs<DT>(a, 16 * MT, NT * kPer, kPer, kThreads, [&](const MxLinearArgs &b, int rows, int cols) {
         mx_linear_direct_kernel<DT, FMT, MT, NT>
-            <<<dim3((uint32_t)rows * cols * kPer), 64 * kDirectWaves, 0, s>>>(b, mx_grid(rows, cols * kPer));
+            <<<dim3((uint32_t)rows * cols * kPer), kThreads, 0, s>>>(b, mx_grid(rows, cols * kPer));
     });
 }
 
@@ -592,9 +594,10 @@ template <int DT, int FMT, int RW, int MT, int FW, int NT, int KW>
 void linear_tiles(const MxLinearArgs &a, hipStream_t s)
 {
     typedef MxTile<DT, FMT, RW, MT, FW, NT, KW> T;
-    by_row_slabs<DT>(a, T::kRows, T::kTiles, [&](const MxLinearArgs &b, int rows, int cols) {
+    constexpr int kThreads = 64 * T::kSet * KW;
+    by_row_slabs<DT>(a, T::kRows, T::kTiles, 1, kThreads, [&](const MxLinearArgs &b, int rows, int cols) {
         mx_linear_tile_kernel<DT, FMT, RW, MT, FW, NT, KW>
-            <<<dim3((uint32_t)rows * cols), 64 * T::kSet * KW, 0, s>>>(b, mx_grid(rows, cols));
+            <<<dim3((uint32_t)rows * cols), kThreads, 0, s>>>(b, mx_grid(rows, cols));
     });
 }
 

@@ -267,7 +267,7 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
 {
     __shared__ double part[T / 64];
     const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
+    const int64_t row = a.row0 + blockIdx.x;
     const int units = (int)((a.k + kMxChunk - 1) / kMxChunk) * (kMxChunk / 8);
     Vec8<DT> vx[NU], vr[NU];
 #pragma unroll
@@ -352,9 +352,12 @@ template <class F> hipError_t by_slabs(MxRowArgs a, int64_t n_rows, int per_thre
     return hipGetLastError();
 }
 
-template <int DT, int NU, int T> void norm_go(const MxNormArgs &a, hipStream_t s)
+template <int DT, int NU, int T> void norm_go(MxNormArgs a, hipStream_t s)
 {
-    rmsnorm_mx_kernel<DT, NU, T><<<dim3((uint32_t)a.n_rows), dim3(T), 0, s>>>(a);
+    for_slabs(a.n_rows, slab_rows(1, 1, T), [&](int64_t row0, int64_t rows) {
+        a.row0 = row0;
+        rmsnorm_mx_kernel<DT, NU, T><<<dim3((uint32_t)rows), dim3(T), 0, s>>>(a);
+    });
 }
 
 template <int DT> void norm_pick(const MxNormArgs &a, hipStream_t s)
