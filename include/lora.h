@@ -500,8 +500,9 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
  * its own side), and h_j^2 is summed in 64 bits.  weight: DEVICE [k], dtype.
  * out, h_out, and q with s may each be NULL, not all of them.  h_out and out
  * may be x or residual themselves with the same stride (in place); otherwise
- * the outputs overlap nothing.  eps >= 0.  A row whose h_j^2 all vanish and
- * eps == 0 gives NaN.  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ * the outputs overlap nothing.  eps >= 0.  Rows of every finite size have their
+ * value, also where h_j^2 is outside fp32's range; a row of zeros with eps == 0
+ * gives NaN.  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
  */
 lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
                             void *h_out, int64_t ldh, const void *x, int64_t ldx,

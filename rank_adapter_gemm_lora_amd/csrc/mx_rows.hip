@@ -222,13 +222,22 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b
             sc[j & 3] = 0;
 }
 
-// 1 / sqrt(m) as a sum x + y: the hardware's reciprocal root (within 2^-23; small
-// m scaled, it would be flushed), one Newton step on m's high and low parts, and
-// what rounding that step loses.  y is 0 where m is 0 or not finite.
-__device__ __forceinline__ float2 mx_inv_sqrt(double m)
+// (x + y) 2^e = 1 / sqrt(m): the hardware's reciprocal root (within 2^-23), one
+// Newton step on m's high and low parts, and what rounding that step loses.  An m
+// that is, or whose root is, near the ends of fp32's range is brought to [1/4, 1) by
+// an even power of two first; its root's power is left for h (a mean square of 2^250
+// has a root, but no fp32 square).  y and e are 0 where m is 0 or not finite.
+struct MxRoot {
+    float x, y;
+    int e;
+};
+__device__ __forceinline__ MxRoot mx_inv_sqrt(double m)
 {
-    const bool tiny = m < 0x1p-96;
-    m *= tiny ? 0x1p64 : 1.;
+    int e = 0;
+    if (!(m >= 0x1p-96 && m < 0x1p96)) {
+        e = -((__builtin_amdgcn_frexp_exp(m) + 1) >> 1);
+        m = __builtin_ldexp(m, 2 * e);
+    }
     const float hi = (float)m, lo = (float)(m - hi);
     const float r = __builtin_amdgcn_rsqf(hi);
     float x = r, y = 0.f;
@@ -238,8 +247,7 @@ __device__ __forceinline__ float2 mx_inv_sqrt(double m)
         x = fmaf(0.5f * r, left, r);
         y = fmaf(0.5f * r, left, -(x - r));
     }
-    const float k = tiny ? 0x1p32f : 1.f;
-    return make_float2(x * k, y * k);
+    return MxRoot{x, y, e};
 }
 
 // n + l (l under half a step of n) rounded to odd: towards zero, then the last
@@ -306,7 +314,8 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
         for (int w = 0; w < T / 64; ++w)
             sum += part[w];
     }
-    const float2 inv = mx_inv_sqrt(sum * a.inv_k + a.eps);
+    const MxRoot inv = mx_inv_sqrt(sum * a.inv_k + a.eps);
+    const int far = __builtin_amdgcn_readfirstlane(inv.e);   // the same in every lane
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
         const int unit = tid + T * j;
@@ -323,8 +332,9 @@ __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
                 // h inv w and what its roundings lose: n is near the once-rounded
                 // value, and its codes are taken of n + lost, not of n.  (A product
                 // that is not finite stands without the lost part.)
-                const float p = f[j][e] * inv.x, pw = p * w[e];
-                const float l = fmaf(f[j][e], inv.x, -p) + f[j][e] * inv.y;
+                const float fj = __builtin_ldexpf(f[j][e], far);
+                const float p = fj * inv.x, pw = p * w[e];
+                const float l = fmaf(fj, inv.x, -p) + fj * inv.y;
                 n[e] = fabsf(pw) < INFINITY ? fmaf(p, w[e], l * w[e]) : pw;
                 f[j][e] = mx_to_odd(n[e], fmaf(l, w[e], fmaf(p, w[e], -n[e])));
             }
