@@ -23,3 +23,15 @@ def test_split_a_binade_lower_shows():
     x, w = C.wide_products(33, 264, 40, 3)
     high = np.where(np.abs(x) >= 1, x, 0)
     assert (C.instruction(high, w) + C.instruction(x - high, w) != x @ w.T).any(1).mean() > 0.5
+
+
+def test_squares_summed_in_32_bits_show():
+    """A norm whose squares are summed in fp32 leaves the bound of the norm's precision tests."""
+    g = np.random.default_rng(1)
+    x = g.standard_normal((16, 4096)).astype(np.float32)
+    _, want = R.norm(x.astype(np.float64), None, np.ones(4096), 0.0)
+    mean = np.float32(1 / 4096) * np.cumsum((x * x).reshape(16, 64, 64), -1, dtype=np.float32)[..., -1].sum(-1, dtype=np.float32)
+    got = (x / np.sqrt(mean.astype(np.float64))[:, None]).astype(np.float32)
+    near = 2.0 ** -40
+    off = np.abs(got - want) > (2.0 ** -24 * (1 + near) + near) * np.abs(want)
+    assert off.any(1).mean() > 0.5
