@@ -516,7 +516,8 @@ lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *
  *
  *      a = g / (1 + exp(-g)) * u,   out = round(a),  (q, s) = a in e4m3 blocks
  *
- * each rounded once from the fp32 a.  out, or q with s, may be NULL, not both.
+ * a in fp32 operations one by one (exp(-g) is infinite below g = -88.7, and a then
+ * 0), each output rounded once from it.  out, or q with s, may be NULL, not both.
  * Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
  */
 lora_status lora_swiglu_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,

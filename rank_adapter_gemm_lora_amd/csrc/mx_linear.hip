@@ -134,8 +134,9 @@ template <int N, class F> __device__ __forceinline__ void mx_for(F f)
 // X as 16 rows' pieces of 16 bytes): nothing is shared between wavefronts, so
 // there is no LDS traffic and no barrier in the loop.  A wavefront holds four
 // chunks; each is refilled with the next group's as soon as it is multiplied.
-// Bound by the stream of W and by what a launch costs: 1 x 4096 x 6144 4.9 us
-// (13.4 MB), 1 x 14336 x 4096 7.2 us (31 MB at 4.3 TB/s), 64 x 4096 x 4096 6.3 us.
+// Bound by the stream of W and by what a launch costs: 1 x 4096 x 6144 4.1 us with
+// its 13.4 MB in the caches and 5.9 us where 64 weights take turns (857 MB);
+// 1 x 14336 x 4096 7.2 us (31 MB at 4.3 TB/s), 64 x 4096 x 4096 6.3 us, in the caches.
 constexpr int kDirectWaves = 8;
 
 template <int FMT, int MT, int NT> struct MxChunk {
@@ -611,9 +612,10 @@ void linear_tiles(const MxLinearArgs &a, hipStream_t s)
 //   512 x 14336 x 4096   64x64 (512)           57      64x128 (256) 44    128x256 (64) 147
 // (up to 16 rows twice as many: larger tiles only add features there;
 //   8 x 4096 x 28672     16x64 (448)           12.2    64x128 (224) 15.3).
-// Beyond one round, 64x128 with k in one piece, four workgroups a CU, until the
-// largest tile's rounds (two workgroups a CU in 8 bits, one in 4 bits) are well
-// filled (a CU left with one of two runs it in 4/7 of the pair's time):
+// Beyond one round, 64x128 with k in one piece, four workgroups a CU (three in 4
+// bits, whose two chunks a stage take 51 KB of LDS), until the largest tile's
+// rounds (two workgroups a CU in 8 bits, one in 4 bits) are well filled (a CU left
+// with one of two runs it in 4/7 of the pair's time):
 //   1024 x 4096 x 6144   64x128 39.0   128x256 (192 workgroups) 47.6
 //   20000 x 1024 x 1024  64x128 35.7   128x256 (628)            38.8
 //   4096 x 4096 x 6144   64x128 134    128x256 (768)            126

@@ -264,12 +264,15 @@ __device__ __forceinline__ float mx_to_odd(float n, float l)
 
 // One row per workgroup of T threads; the row stays in registers, NU units of 8
 // a thread (unit t + T j), so x and the residual are read once and nothing is
-// written before the whole row is in.
+// written before the whole row is in.  (fp32 rows past 32768, eight units a thread
+// of 1024, go over the 128 registers of a lane: 64 bytes of each are kept in
+// scratch.  64 x 65536: 27 us.)
 // The squares are summed in 64 bits, so that the codes of n + lost are the exact
 // value's but for its last bits: none of 4.3 M differed (fp32 sums: 4, and codes
-// of the rounded n: 7).  35422 x 4096 bf16: 226 - 232 us, 1.3 GB at 5.7 TB/s,
-// and as long without either; 300 x 14336, one to two rows a CU and bound by
-// their instructions: 16.0 us with its inverse, 14.9 without.
+// of the rounded n: 7).  35422 x 4096 bf16: 225 - 228 us, 1.3 GB at 5.7 TB/s,
+// and as long with fp32 sums and codes; 300 x 14336, one to two rows a CU and bound
+// by their instructions: 11.2 us (a pass with its inverse 16.0 us; with fp32 sums
+// and codes 14.9).
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void rmsnorm_mx_kernel(MxNormArgs a)
 {
