@@ -417,8 +417,8 @@ lora_status lora_build_apply_plan(const lora_stack *st, int64_t n_rows, const lo
  * n_rows 0 checks its arguments' values and does nothing.  All sums are fp32
  * or wider.
  * Nothing is allocated per call, and every call can be captured in a HIP
- * graph.  Limits: k <= 2^20 (lora_rmsnorm_mx: 2^16), d <= 2^22, n_rows <
- * 2^30; beyond them LORA_E_UNSUPPORTED.
+ * graph.  Limits: k <= 2^20 (lora_rmsnorm_mx: 2^16, lora_block_norm_mx: 2^15),
+ * d <= 2^22, n_rows < 2^30; beyond them LORA_E_UNSUPPORTED.
  */
 typedef enum lora_mx_format { LORA_MX_E4M3 = 0, LORA_MX_E2M1 = 1 } lora_mx_format;
 
@@ -523,6 +523,30 @@ lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *
 lora_status lora_swiglu_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
                            const void *gu, int64_t ldg, lora_dtype dtype, int64_t n_rows,
                            int64_t f, void *stream);
+
+/*
+ * What stands between two blocks: the norm of a block's output y, its gate and
+ * residual scale, the residual sum, and the next block's norm in two forms, from
+ * one pass:
+ *
+ *      a = y * (mean_j y_j^2 + eps)^-1/2 * w_post     (w_post NULL: a = y)
+ *      h = residual + scale * gate * a                (residual NULL: 0; gate NULL: 1)
+ *      n = h * (mean_j h_j^2 + eps)^-1/2 * w_pre
+ *      h_out = round(h),  out = round(n),  (q, s) = n in e4m3 blocks
+ *
+ * all in 64 bits, n from the unrounded h, each output rounded once.  w_post,
+ * w_pre: DEVICE [k], dtype.  gate: DEVICE, dtype, [n_rows][ldg], or one row [k]
+ * for all with ldg == 0.  out, h_out, and q with s may each be NULL, not all of
+ * them; w_pre may be NULL if out and q are.  h_out and out may be y or residual
+ * themselves with the same stride (in place); otherwise the outputs overlap
+ * nothing.  eps >= 0, scale finite.  A row of zeros under a norm with eps == 0
+ * gives NaN.  k <= 2^15.  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+lora_status lora_block_norm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
+                               void *h_out, int64_t ldh, const void *y, int64_t ldy,
+                               const void *residual, int64_t ldr, const void *w_post,
+                               const void *gate, int64_t ldg, float scale, const void *w_pre,
+                               float eps, lora_dtype dtype, int64_t n_rows, int64_t k, void *stream);
 
 /* --------------------------------------------------------------- residency */
 

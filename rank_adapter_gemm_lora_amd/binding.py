@@ -36,7 +36,7 @@ EXPORTS = ("lora_stack_create", "lora_stack_destroy", "lora_load_slot", "lora_ev
            "lora_build_apply_noalloc", "lora_build_apply_plan",
            "lora_mx_quantize", "lora_mx_dequantize", "lora_mx_weight_create",
            "lora_mx_weight_destroy", "lora_mx_weight_load", "lora_mx_weight_load_packed",
-           "lora_mx_linear", "lora_rmsnorm_mx", "lora_swiglu_mx",
+           "lora_mx_linear", "lora_rmsnorm_mx", "lora_swiglu_mx", "lora_block_norm_mx",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_register",
            "lora_residency_unregister", "lora_residency_map_batch", "lora_residency_slot_of",
            "lora_residency_stats",
@@ -111,6 +111,8 @@ def load(path: str | None = None):
             "lora_rmsnorm_mx": [P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, F, I, I64,
                                 I64, P],
             "lora_swiglu_mx": [P, I64, P, I64, P, I64, P, I64, I, I64, I64, P],
+            "lora_block_norm_mx": [P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, I64, F, P,
+                                   F, I, I64, I64, P],
             "lora_residency_create": [PP, P, I, I, I64, I, P, I, I],
             "lora_residency_destroy": [P],
             "lora_residency_register": [P, I64, I, F, P, P],
@@ -347,6 +349,16 @@ def lora_swiglu_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, gu: i
     st = (_lib or load()).lora_swiglu_mx(out, ldo, q, ldq, s, lds, gu, ldg, dtype, n_rows, f, stream)
     if st:
         _check(st, "lora_swiglu_mx")
+
+
+def lora_block_norm_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, h_out: int, ldh: int,
+                       y: int, ldy: int, residual: int, ldr: int, w_post: int, gate: int, ldg: int,
+                       scale: float, w_pre: int, eps: float, dtype: int, n_rows: int, k: int,
+                       stream=None):
+    """Pointers of outputs, residual, gate and weights may be 0 (not wanted / none)."""
+    st = (_lib or load()).lora_block_norm_mx(out, ldo, q, ldq, s, lds, h_out, ldh, y, ldy, residual, ldr, w_post, gate, ldg, scale, w_pre, eps, dtype, n_rows, k, stream)
+    if st:
+        _check(st, "lora_block_norm_mx")
 
 
 def lora_residency_create(stack, max_cpu_adapters: int, n_slots: int = 0, r_max: int = 0,

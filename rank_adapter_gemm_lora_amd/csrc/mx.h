@@ -12,6 +12,7 @@ namespace lora {
 
 constexpr int64_t kMxMaxK = (int64_t)1 << 20;       // inputs of a row in blocks
 constexpr int64_t kMxMaxNormK = (int64_t)1 << 16;   // a norm's row stays in one workgroup's registers
+constexpr int64_t kMxMaxBlockNormK = (int64_t)1 << 15;   // the same, in 64 bits
 constexpr int64_t kMxMaxD = (int64_t)1 << 22;
 constexpr int64_t kMxMaxRows = (int64_t)1 << 30;
 
@@ -77,6 +78,28 @@ struct MxNormArgs {
     int64_t k;
 };
 hipError_t launch_rmsnorm_mx(int dtype, const MxNormArgs &a, hipStream_t s);
+
+struct MxBlockNormArgs {
+    const void *y;
+    int64_t ldy;
+    const void *res;     // or null
+    int64_t ldr;
+    const void *post;    // or null: y stands as it is
+    const void *gate;    // or null
+    int64_t ldg;         // 0: one row for all
+    const void *pre;     // or null: h alone
+    double scale, eps;
+    double inv_k;        // 1 / k
+    void *h;             // or null
+    int64_t ldh;
+    void *out;           // or null
+    int64_t ldo;
+    MxBlocks b;          // b.q null: not wanted
+    int64_t row0;        // first row of this launch
+    int64_t n_rows;
+    int64_t k;
+};
+hipError_t launch_block_norm_mx(int dtype, const MxBlockNormArgs &a, hipStream_t s);
 
 // The weight image.  Output features are cut into tiles of 16, k into chunks of
 // 128; per (tile, chunk) the codes are one kilobyte in matrix-core operand

@@ -257,3 +257,45 @@ lora_status lora_swiglu_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s
     a.k = f;
     return status_of(launch_swiglu_mx(dt_of(dtype), a, n_rows, stream_of(stream)));
 }
+
+lora_status lora_block_norm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
+                               void *h_out, int64_t ldh, const void *y, int64_t ldy,
+                               const void *residual, int64_t ldr, const void *w_post,
+                               const void *gate, int64_t ldg, float scale, const void *w_pre,
+                               float eps, lora_dtype dtype, int64_t n_rows, int64_t k, void *stream)
+{
+    if (!dtype_ok(dtype) || !(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return LORA_E_ARG;
+    const lora_status st = check_shape(n_rows, k, kMxMaxBlockNormK);
+    if (st != LORA_OK)
+        return st;
+    if ((!out && !q && !h_out) || !q != !s || (!w_pre && (out || q)) ||
+        !dense_ok(y, ldy, k, n_rows) || (residual && !dense_ok(residual, ldr, k, n_rows)) ||
+        (w_post && !aligned16(w_post)) || (w_pre && !aligned16(w_pre)) ||
+        (gate && !(ldg == 0 ? aligned16(gate) : dense_ok(gate, ldg, k, n_rows))) ||
+        (h_out && !dense_ok(h_out, ldh, k, n_rows)) || (out && !dense_ok(out, ldo, k, n_rows)) ||
+        (q && !blocks_ok(q, ldq, s, lds, LORA_MX_E4M3, k, n_rows)))
+        return LORA_E_ARG;
+    if (n_rows == 0)
+        return LORA_OK;
+    MxBlockNormArgs a{};
+    a.y = y;
+    a.ldy = ldy;
+    a.res = residual;
+    a.ldr = ldr;
+    a.post = w_post;
+    a.gate = gate;
+    a.ldg = ldg;
+    a.pre = w_pre;
+    a.scale = scale;
+    a.eps = eps;
+    a.inv_k = 1. / (double)k;
+    a.h = h_out;
+    a.ldh = ldh;
+    a.out = out;
+    a.ldo = ldo;
+    a.b = blocks_of(q, ldq, s, lds);
+    a.n_rows = n_rows;
+    a.k = k;
+    return status_of(launch_block_norm_mx(dt_of(dtype), a, stream_of(stream)));
+}

@@ -1,0 +1,31 @@
+"""The block norm's, the router's and the experts' calls refuse bad arguments on the host, before any GPU call
+(runs without one: pointers are made-up addresses that are never read)."""
+import pytest
+
+from rank_adapter_gemm_lora_amd import binding as lb
+from test_mx_refusals import BF, P, _args, refused
+
+NN = ("out", "ldo", "q", "ldq", "s", "lds", "h", "ldh", "y", "ldy", "r", "ldr", "post", "gate", "ldg", "scale", "pre", "eps",
+      "dtype", "n", "k")
+NB = (P, 104, P, 128, P, 16, P, 104, P, 104, P, 104, P, P, 104, 1.0, P, 1e-5, BF, 4, 104)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"out": 0, "q": 0, "s": 0, "h": 0}, lb.LORA_E_ARG), ({"q": 0}, lb.LORA_E_ARG), ({"s": 0}, lb.LORA_E_ARG),
+    ({"y": 0}, lb.LORA_E_ARG), ({"pre": 0}, lb.LORA_E_ARG), ({"pre": 0, "out": 0}, lb.LORA_E_ARG),
+    ({"pre": 0, "q": 0, "s": 0}, lb.LORA_E_ARG), ({"pre": P + 4}, lb.LORA_E_ARG), ({"post": P + 8}, lb.LORA_E_ARG),
+    ({"gate": P + 2}, lb.LORA_E_ARG), ({"gate": P + 2, "ldg": 0}, lb.LORA_E_ARG), ({"ldg": 96}, lb.LORA_E_ARG),
+    ({"ldg": -104}, lb.LORA_E_ARG), ({"ldg": 108}, lb.LORA_E_ARG), ({"eps": -1.0}, lb.LORA_E_ARG),
+    ({"eps": float("nan")}, lb.LORA_E_ARG), ({"scale": float("inf")}, lb.LORA_E_ARG), ({"scale": float("nan")}, lb.LORA_E_ARG),
+    ({"ldy": 96}, lb.LORA_E_ARG), ({"ldr": 100}, lb.LORA_E_ARG), ({"ldh": 108}, lb.LORA_E_ARG), ({"ldo": 0}, lb.LORA_E_ARG),
+    ({"out": P + 8}, lb.LORA_E_ARG), ({"h": P + 8}, lb.LORA_E_ARG), ({"r": P + 8}, lb.LORA_E_ARG), ({"ldq": 64}, lb.LORA_E_ARG),
+    ({"lds": 8}, lb.LORA_E_ARG), ({"k": 12}, lb.LORA_E_ARG), ({"k": 0}, lb.LORA_E_ARG), ({"n": -2}, lb.LORA_E_ARG),
+    ({"dtype": 2}, lb.LORA_E_ARG), ({"ldy": 1 << 60}, lb.LORA_E_ARG), ({"n": 1 << 30}, lb.LORA_E_UNSUPPORTED),
+    ({"k": (1 << 15) + 8}, lb.LORA_E_UNSUPPORTED),
+])
+def test_block_norm_refuses(change, status):
+    refused(lb.lora_block_norm_mx, _args(NN, NB, change), status)
+
+
+def test_block_norm_without_rows():
+    lb.lora_block_norm_mx(P, 104, 0, 0, 0, 0, 0, 0, 0, 104, 0, 0, 0, 0, 0, 1.0, P, 0.0, BF, 0, 104)
