@@ -53,28 +53,26 @@ template <int T> __device__ __forceinline__ double block_sum(double v, double *p
     return v;
 }
 
-// v as its nearest float, and rounded to odd: what a shorter format is rounded
-// from so that the result is v's own rounding.
-struct MxOnce {
-    float near, odd;
-};
-__device__ __forceinline__ MxOnce mx_once(double v)
+// v as a float that rounds to bf16 or a code as v itself does: 21 bits of v, the
+// last one set where anything below it is (rounded to odd), which a float holds
+// exactly (under 2^-126 the float's own rounding comes first).
+__device__ __forceinline__ float mx_odd_of(double v)
 {
-    const float n = (float)v;
-    return MxOnce{n, mx_to_odd(n, (float)(v - (double)n))};
-}
-template <int DT> __device__ __forceinline__ float mx_stored(const MxOnce &o)
-{
-    return DT == DT_F32 ? o.near : o.odd;
+    const int64_t b = __double_as_longlong(v);
+    const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32) | min(lo, 1u);
+    float f = (float)__longlong_as_double((int64_t)((uint64_t)hi << 32));
+    asm("" : "+v"(f));   // or the compiler joins the two conversions into a longer one of its own
+    return f;
 }
 
 // One row per workgroup of T threads, NU units of 8 elements a thread (unit t +
 // T j).  All of a row is loaded before anything is written, so outputs may
 // replace inputs.  Everything between the loads and the stores is in 64 bits
-// (the vector units run 64-bit products and sums at the 32-bit ones' rate): h
-// and n then differ from their exact values by some 2^-50, and each output is
-// that value rounded once.  Up to two units a thread the weights come with the
-// row, ahead of the sums; beyond, the registers would not hold them.
+// (the vector units run 64-bit products and sums at the 32-bit ones' rate; the
+// product of a bf16 weight and a bf16 gate is exact in 32): h and n then differ
+// from their exact values by some 2^-50, and each output is that value rounded
+// once.  Up to two units a thread the weights come with the row, ahead of the
+// sums; beyond, the registers would not hold them.
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
 {
@@ -87,15 +85,12 @@ __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
         const int64_t c = (int64_t)(tid + T * j) * 8;
-        vy[j].zero();
-        vr[j].zero();
-        vg[j].zero();
-        vpost[j].zero();
-        vpre[j].zero();
         if (c < a.k) {
             vy[j].load(a.y, row * a.ldy + c);
             if (a.res)
                 vr[j].load(a.res, row * a.ldr + c);
+            else
+                vr[j].zero();
             if (a.gate)
                 vg[j].load(a.gate, row * a.ldg + c);
             if (kEarly && a.post)
@@ -104,40 +99,62 @@ __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
                 vpre[j].load(a.pre, c);
         }
     }
+    double h[NU][8];   // y first
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+        float f[8];
+        vy[j].to_f32(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[j][e] = (double)f[e];
+    }
     double by = a.scale;   // what y is multiplied by next to its weight and gate
     if (a.post) {
         double sum = 0.;
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
-            float f[8];
-            vy[j].to_f32(f);
+            if ((int64_t)(tid + T * j) * 8 < a.k) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum = fma((double)f[e], (double)f[e], sum);
+                for (int e = 0; e < 8; ++e)
+                    sum = fma(h[j][e], h[j][e], sum);
+            }
         }
         by *= rsqrt(block_sum<T>(sum, part[0]) * a.inv_k + a.eps);
     }
-    double h[NU][8], sum = 0.;
+    double sum = 0.;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
         const int64_t c = (int64_t)(tid + T * j) * 8;
-        if (!kEarly && a.post && c < a.k)
-            vpost[j].load(a.post, c);
-        float y[8], r[8], g[8], w[8];
-        vy[j].to_f32(y);
-        vr[j].to_f32(r);
-        vg[j].to_f32(g);
-        vpost[j].to_f32(w);
+        if (c < a.k) {
+            if (!kEarly && a.post)
+                vpost[j].load(a.post, c);
+            float r[8];
+            vr[j].to_f32(r);
+            if (a.post && a.gate) {
+                float g[8], w[8];
+                vg[j].to_f32(g);
+                vpost[j].to_f32(w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            double m = by * (double)y[e];
-            if (a.post)
-                m *= (double)w[e];
-            if (a.gate)
-                m *= (double)g[e];
-            h[j][e] = m + (double)r[e];
-            // threads past the row's end add nothing, also where by is not finite
-            if (c < a.k)
+                for (int e = 0; e < 8; ++e) {
+                    const double m = DT == DT_BF16 ? (double)(w[e] * g[e]) : (double)w[e] * (double)g[e];
+                    h[j][e] = fma(by * h[j][e], m, (double)r[e]);
+                }
+            } else if (a.post || a.gate) {
+                float w[8];
+                if (a.post)
+                    vpost[j].to_f32(w);
+                else
+                    vg[j].to_f32(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[j][e] = fma(by * h[j][e], (double)w[e], (double)r[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[j][e] = fma(by, h[j][e], (double)r[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
                 sum = fma(h[j][e], h[j][e], sum);
         }
     }
@@ -149,15 +166,12 @@ __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
         const int unit = tid + T * j;
         const int64_t c = (int64_t)unit * 8;
         float n[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            n[e] = 0.f;
         if (c < a.k) {
             float f[8], w[8];
             if (a.h) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    f[e] = mx_stored<DT>(mx_once(h[j][e]));
+                    f[e] = DT == DT_F32 ? (float)h[j][e] : mx_odd_of(h[j][e]);
                 Vec8<DT>::store(a.h, row * a.ldh + c, f);
             }
             if (a.pre) {
@@ -166,13 +180,17 @@ __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
                 vpre[j].to_f32(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const MxOnce o = mx_once(h[j][e] * inv * (double)w[e]);
-                    n[e] = o.odd;
-                    f[e] = mx_stored<DT>(o);
+                    const double v = h[j][e] * inv * (double)w[e];
+                    n[e] = mx_odd_of(v);
+                    f[e] = DT == DT_F32 ? (float)v : n[e];
                 }
                 if (a.out)
                     Vec8<DT>::store(a.out, row * a.ldo + c, f);
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                n[e] = 0.f;
         }
         if (a.b.q && unit < units)   // whole 16-lane groups
             mx_store_unit<LORA_MX_E4M3>(a.b.q + row * a.b.ldq, a.b.s + row * a.b.lds, unit, units, n);

@@ -84,18 +84,6 @@ __device__ __forceinline__ typename MxFmt<FMT>::unit_t mx_codes(const float (&f)
     }
 }
 
-// n + l (l under half a step of n) rounded to odd: towards zero, then the last
-// bit set; n itself if l is 0 or not finite.  Rounding that to a shorter format
-// gives what n + l itself rounds to, which n would not on a border (l decides).
-// l is 0 where n is: the sign's subtraction never passes 0.
-__device__ __forceinline__ float mx_to_odd(float n, float l)
-{
-    constexpr int kFiniteNotZero = 0x198;   // normals and subnormals of either sign
-    const int b = __float_as_int(n);
-    const int odd = (b + ((__float_as_int(l) ^ b) >> 31)) | 1;
-    return __int_as_float(__builtin_amdgcn_classf(l, kFiniteNotZero) ? odd : b);
-}
-
 // Write this lane's unit of a row in blocks: 8 codes, and from the first lane
 // of each 16 (128 elements, four blocks) the four scale bytes as one word; the
 // row's last such lane also writes the padding words.  unit: 0 .. units - 1, a

@@ -250,6 +250,18 @@ __device__ __forceinline__ MxRoot mx_inv_sqrt(double m)
     return MxRoot{x, y, e};
 }
 
+// n + l (l under half a step of n) rounded to odd: towards zero, then the last
+// bit set; n itself if l is 0 or not finite.  Rounding that to a shorter format
+// gives what n + l itself rounds to, which n would not on a border (l decides).
+// l is 0 where n is: the sign's subtraction never passes 0.
+__device__ __forceinline__ float mx_to_odd(float n, float l)
+{
+    constexpr int kFiniteNotZero = 0x198;   // normals and subnormals of either sign
+    const int b = __float_as_int(n);
+    const int odd = (b + ((__float_as_int(l) ^ b) >> 31)) | 1;
+    return __int_as_float(__builtin_amdgcn_classf(l, kFiniteNotZero) ? odd : b);
+}
+
 // One row per workgroup of T threads; the row stays in registers, NU units of 8
 // a thread (unit t + T j), so x and the residual are read once and nothing is
 // written before the whole row is in.  (fp32 rows past 32768, eight units a thread
