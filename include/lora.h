@@ -548,6 +548,92 @@ lora_status lora_block_norm_mx(void *out, int64_t ldo, void *q, int64_t ldq, voi
                                const void *gate, int64_t ldg, float scale, const void *w_pre,
                                float eps, lora_dtype dtype, int64_t n_rows, int64_t k, void *stream);
 
+/* --------------------------------------------------------- mixture layers */
+
+/*
+ * A mixture layer sends every row through top_k of its experts and adds up
+ * what they return.  Pair p = i * top_k + j is choice j of row i.  The calls
+ * below choose the experts (or take the caller's choice), group the pairs by
+ * expert as lora_build_segments groups rows by adapter, and bring the pairs'
+ * results back to their rows.
+ *
+ * Limits: n_experts <= LORA_MAX_EXPERTS, top_k <= LORA_MAX_TOP_K, n_rows * top_k
+ * <= 2^30.
+ */
+#define LORA_MAX_EXPERTS 1024
+#define LORA_MAX_TOP_K 16
+
+typedef struct lora_moe_plan lora_moe_plan; /* owns one batch's grouping by expert */
+
+typedef enum lora_moe_score { LORA_MOE_SOFTMAX = 0, LORA_MOE_SIGMOID = 1 } lora_moe_score;
+
+/*
+ * Create a plan for up to max_rows rows of top_k <= n_experts choices each.
+ * Allocates device memory on the current HIP device; all later calls must run
+ * with that device current.  A plan holds one grouping at a time: calls that
+ * use it must not overlap with one that writes it, and a graph captured with a
+ * plan belongs to the number of rows it was captured with.  Errors: LORA_E_ARG,
+ * LORA_E_UNSUPPORTED, LORA_E_NOMEM, LORA_E_HIP.
+ */
+lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_experts, int top_k);
+
+/* Free a plan (NULL is accepted); synchronises the device first. */
+lora_status lora_moe_plan_destroy(lora_moe_plan *plan);
+
+/*
+ * Choose each row's experts from its logits and group the pairs.
+ *
+ *   logits  DEVICE [n_rows][ldl], dtype; ldl >= n_experts, any alignment of
+ *           whole elements.  An expert whose logit is -infinity or NaN is
+ *           switched off for the row.
+ *   ids     DEVICE int32 [n_rows][top_k]: the experts with the largest logits,
+ *           largest first, the lower number first among equal ones; -1 where no
+ *           more experts are left
+ *   weights DEVICE float [n_rows][top_k]: scale * p, 0 beside an id of -1.
+ *           LORA_MOE_SOFTMAX: p = exp(l - max) / sum over all experts of the
+ *           row, or over its chosen ones if renormalize != 0 (of infinite
+ *           logits each counts 1).  LORA_MOE_SIGMOID: p = 1 / (1 + exp(-l)),
+ *           divided by the chosen ones' sum if renormalize != 0.  In fp32.
+ *   order   DEVICE int32 [n_rows * top_k] or NULL: the pairs sorted by expert,
+ *           by pair inside a group, those without an expert last
+ *   offsets DEVICE int32 [n_experts + 1] or NULL: the first position of each
+ *           group in that order; the last is the number of pairs with an expert
+ *
+ * order and offsets are copies: the plan keeps its own.  The launches depend on
+ * sizes alone.  n_rows 0 .. max_rows.  Errors: LORA_E_ARG, LORA_E_HIP.
+ */
+lora_status lora_moe_route(lora_moe_plan *plan, int32_t *ids, float *weights, int32_t *order,
+                           int32_t *offsets, const void *logits, int64_t ldl, lora_dtype dtype,
+                           int64_t n_rows, lora_moe_score score, int renormalize, float scale,
+                           void *stream);
+
+/*
+ * Group the pairs by the caller's own choice, ids DEVICE int32 [n_rows][top_k];
+ * an id outside [0, n_experts) is no expert.  A row may name an expert twice.
+ * order and offsets as above.  Errors: LORA_E_ARG, LORA_E_HIP.
+ */
+lora_status lora_moe_group(lora_moe_plan *plan, const int32_t *ids, int64_t n_rows, int32_t *order,
+                           int32_t *offsets, void *stream);
+
+/*
+ * Bring the pairs' results back to their rows:
+ *
+ *      out[i] = round(residual[i] + sum_j weights[i][j] * y[position of pair (i, j)])
+ *
+ * over the pairs that have an expert, in the order of j, in fp32, rounded once.
+ *   y        [n_rows * top_k][ldy], rows in the grouped order; rows of pairs
+ *            without an expert are not read
+ *   weights  DEVICE float [n_rows][top_k]
+ *   residual [n_rows][ldr] or NULL (0); may be out itself with the same stride
+ * d columns (a multiple of 8, at most 2^22), dense matrices as above.  Rows are
+ * those of the last lora_moe_route / lora_moe_group of the plan.  Errors:
+ * LORA_E_ARG, LORA_E_EMPTY (nothing was grouped yet), LORA_E_UNSUPPORTED,
+ * LORA_E_HIP.
+ */
+lora_status lora_moe_combine(const lora_moe_plan *plan, void *out, int64_t ldo, const void *y,
+                             int64_t ldy, const float *weights, const void *residual, int64_t ldr,
+                             lora_dtype dtype, int64_t d, void *stream);
+
 /* --------------------------------------------------------------- residency */
 
 /*

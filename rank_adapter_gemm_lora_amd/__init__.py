@@ -19,4 +19,6 @@ from .binding import (EXPORTS, LORA_BF16, LORA_F32, LORA_MX_E2M1, LORA_MX_E4M3, 
                       lora_mx_code_bytes, lora_mx_scale_bytes, lora_mx_quantize,
                       lora_mx_dequantize, lora_mx_weight_create, lora_mx_weight_destroy,
                       lora_mx_weight_load, lora_mx_weight_load_packed, lora_mx_linear,
-                      lora_rmsnorm_mx, lora_swiglu_mx, lora_block_norm_mx)
+                      lora_rmsnorm_mx, lora_swiglu_mx, lora_block_norm_mx,
+                      LORA_MOE_SIGMOID, LORA_MOE_SOFTMAX, lora_moe_plan_create,
+                      lora_moe_plan_destroy, lora_moe_route, lora_moe_group, lora_moe_combine)

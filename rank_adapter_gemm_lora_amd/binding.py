@@ -16,6 +16,7 @@ from .build import LIB_PATH
 
 LORA_F32, LORA_BF16 = 0, 1
 LORA_MX_E4M3, LORA_MX_E2M1 = 0, 1
+LORA_MOE_SOFTMAX, LORA_MOE_SIGMOID = 0, 1
 LORA_OK, LORA_E_ARG, LORA_E_RANK, LORA_E_SLOT, LORA_E_OCCUPIED, LORA_E_EMPTY = 0, 1, 2, 3, 4, 5
 LORA_E_NOMEM, LORA_E_HIP, LORA_E_BAD_IDS, LORA_E_UNSUPPORTED = 6, 7, 8, 9
 LORA_E_CAPACITY, LORA_E_NOT_FOUND = 10, 11
@@ -37,6 +38,8 @@ EXPORTS = ("lora_stack_create", "lora_stack_destroy", "lora_load_slot", "lora_ev
            "lora_mx_quantize", "lora_mx_dequantize", "lora_mx_weight_create",
            "lora_mx_weight_destroy", "lora_mx_weight_load", "lora_mx_weight_load_packed",
            "lora_mx_linear", "lora_rmsnorm_mx", "lora_swiglu_mx", "lora_block_norm_mx",
+           "lora_moe_plan_create", "lora_moe_plan_destroy", "lora_moe_route", "lora_moe_group",
+           "lora_moe_combine",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_register",
            "lora_residency_unregister", "lora_residency_map_batch", "lora_residency_slot_of",
            "lora_residency_stats",
@@ -113,6 +116,11 @@ def load(path: str | None = None):
             "lora_swiglu_mx": [P, I64, P, I64, P, I64, P, I64, I, I64, I64, P],
             "lora_block_norm_mx": [P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, P, I64, F, P,
                                    F, I, I64, I64, P],
+            "lora_moe_plan_create": [PP, I64, I, I],
+            "lora_moe_plan_destroy": [P],
+            "lora_moe_route": [P, P, P, P, P, P, I64, I, I64, I, I, F, P],
+            "lora_moe_group": [P, P, I64, P, P, P],
+            "lora_moe_combine": [P, P, I64, P, I64, P, P, I64, I, I64, P],
             "lora_residency_create": [PP, P, I, I, I64, I, P, I, I],
             "lora_residency_destroy": [P],
             "lora_residency_register": [P, I64, I, F, P, P],
@@ -359,6 +367,41 @@ def lora_block_norm_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, h
     st = (_lib or load()).lora_block_norm_mx(out, ldo, q, ldq, s, lds, h_out, ldh, y, ldy, residual, ldr, w_post, gate, ldg, scale, w_pre, eps, dtype, n_rows, k, stream)
     if st:
         _check(st, "lora_block_norm_mx")
+
+
+def lora_moe_plan_create(max_rows: int, n_experts: int, top_k: int):
+    out = ctypes.c_void_p()
+    _check(load().lora_moe_plan_create(ctypes.byref(out), int(max_rows), int(n_experts), int(top_k)),
+           "lora_moe_plan_create")
+    return out
+
+
+def lora_moe_plan_destroy(plan):
+    _check(load().lora_moe_plan_destroy(plan), "lora_moe_plan_destroy")
+
+
+def lora_moe_route(plan, ids: int, weights: int, order: int, offsets: int, logits: int, ldl: int,
+                   dtype: int, n_rows: int, score: int = LORA_MOE_SOFTMAX, renormalize: bool = True,
+                   scale: float = 1.0, stream=None):
+    """order and offsets may be 0 (not wanted)."""
+    st = (_lib or load()).lora_moe_route(plan, ids, weights, order, offsets, logits, ldl, dtype, n_rows, score, renormalize, scale, stream)
+    if st:
+        _check(st, "lora_moe_route")
+
+
+def lora_moe_group(plan, ids: int, n_rows: int, order: int = 0, offsets: int = 0, stream=None):
+    """order and offsets may be 0 (not wanted)."""
+    st = (_lib or load()).lora_moe_group(plan, ids, n_rows, order, offsets, stream)
+    if st:
+        _check(st, "lora_moe_group")
+
+
+def lora_moe_combine(plan, out: int, ldo: int, y: int, ldy: int, weights: int, residual: int,
+                     ldr: int, dtype: int, d: int, stream=None):
+    """residual may be 0 (none)."""
+    st = (_lib or load()).lora_moe_combine(plan, out, ldo, y, ldy, weights, residual, ldr, dtype, d, stream)
+    if st:
+        _check(st, "lora_moe_combine")
 
 
 def lora_residency_create(stack, max_cpu_adapters: int, n_slots: int = 0, r_max: int = 0,

@@ -7,56 +7,9 @@
 #include <cstring>
 #include <new>
 
-#include "mx.h"
+#include "mx_checks.h"
 
 using namespace lora;
-
-namespace {
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool dtype_ok(lora_dtype t) { return t == LORA_F32 || t == LORA_BF16; }
-bool format_ok(lora_mx_format f) { return f == LORA_MX_E4M3 || f == LORA_MX_E2M1; }
-int dt_of(lora_dtype t) { return t == LORA_F32 ? DT_F32 : DT_BF16; }
-hipStream_t stream_of(void *s) { return reinterpret_cast<hipStream_t>(s); }
-
-// Widths and rows: negative or uneven ones are wrong, large ones unsupported.
-lora_status check_shape(int64_t n_rows, int64_t k, int64_t k_max)
-{
-    if (n_rows < 0 || k < 8 || k % 8 != 0)
-        return LORA_E_ARG;
-    return n_rows >= kMxMaxRows || k > k_max ? LORA_E_UNSUPPORTED : LORA_OK;
-}
-
-// A dense matrix of n_rows x width elements with row stride ld; its last
-// element's byte offset must fit 62 bits.
-bool dense_ok(const void *p, int64_t ld, int64_t width, int64_t n_rows)
-{
-    return ld >= width && ld % 8 == 0 && ld < ((int64_t)1 << 58) / (n_rows + 1) &&
-           (n_rows == 0 || (p && aligned16(p)));
-}
-
-bool blocks_ok(const void *q, int64_t ldq, const void *s, int64_t lds, lora_mx_format f, int64_t k,
-               int64_t n_rows)
-{
-    return ldq >= LORA_MX_CODE_BYTES(k, f) && ldq % 16 == 0 && lds >= LORA_MX_SCALE_BYTES(k) &&
-           lds % 16 == 0 && ldq < ((int64_t)1 << 60) / (n_rows + 1) &&
-           lds < ((int64_t)1 << 60) / (n_rows + 1) &&
-           (n_rows == 0 || (q && s && aligned16(q) && aligned16(s)));
-}
-
-MxBlocks blocks_of(const void *q, int64_t ldq, const void *s, int64_t lds)
-{
-    return MxBlocks{static_cast<uint8_t *>(const_cast<void *>(q)), ldq,
-                    static_cast<uint8_t *>(const_cast<void *>(s)), lds};
-}
-
-bool on_device(const lora_mx_weight *w)
-{
-    int cur = -1;
-    return hipGetDevice(&cur) == hipSuccess && cur == w->device;
-}
-
-}  // namespace
 
 lora_status lora_mx_quantize(void *q, int64_t ldq, void *s, int64_t lds, lora_mx_format format,
                              const void *x, int64_t ldx, lora_dtype dtype, int64_t n_rows,
@@ -148,7 +101,7 @@ lora_status lora_mx_weight_destroy(lora_mx_weight *w)
 lora_status lora_mx_weight_load(lora_mx_weight *w, const void *W, int64_t ldw, lora_dtype dtype,
                                 void *stream)
 {
-    if (!w || !dtype_ok(dtype) || !dense_ok(W, ldw, w->w.k, w->w.d) || !on_device(w))
+    if (!w || !dtype_ok(dtype) || !dense_ok(W, ldw, w->w.k, w->w.d) || !on_device(w->device))
         return LORA_E_ARG;
     const lora_status st = status_of(
         launch_mx_image(dt_of(dtype), W, ldw, MxBlocks{}, w->w, stream_of(stream)));
@@ -160,7 +113,7 @@ lora_status lora_mx_weight_load(lora_mx_weight *w, const void *W, int64_t ldw, l
 lora_status lora_mx_weight_load_packed(lora_mx_weight *w, const void *q, int64_t ldq,
                                        const void *s, int64_t lds, void *stream)
 {
-    if (!w || !blocks_ok(q, ldq, s, lds, LORA_MX_E2M1, w->w.k, w->w.d) || !on_device(w))
+    if (!w || !blocks_ok(q, ldq, s, lds, LORA_MX_E2M1, w->w.k, w->w.d) || !on_device(w->device))
         return LORA_E_ARG;
     const lora_status st = status_of(
         launch_mx_image(-1, nullptr, 0, blocks_of(q, ldq, s, lds), w->w, stream_of(stream)));
@@ -179,7 +132,7 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
     if (st != LORA_OK)
         return st;
     if (!dense_ok(y, ldy, w->w.d, n_rows) || !blocks_ok(q, ldq, s, lds, format, w->w.k, n_rows) ||
-        !on_device(w))
+        !on_device(w->device))
         return LORA_E_ARG;
     if (!w->loaded)
         return LORA_E_EMPTY;

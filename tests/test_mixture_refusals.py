@@ -29,3 +29,18 @@ def test_block_norm_refuses(change, status):
 
 def test_block_norm_without_rows():
     lb.lora_block_norm_mx(P, 104, 0, 0, 0, 0, 0, 0, 0, 104, 0, 0, 0, 0, 0, 1.0, P, 0.0, BF, 0, 104)
+
+
+def test_plan_refuses_before_the_device():
+    import ctypes
+    lib = lb.load()
+    out = ctypes.c_void_p()
+    assert lib.lora_moe_plan_destroy(None) == lb.LORA_OK
+    assert lib.lora_moe_plan_create(None, 8, 4, 2) == lb.LORA_E_ARG
+    for rows, experts, top_k in ((0, 4, 2), (-1, 4, 2), (8, 0, 1), (8, 4, 0), (8, 4, 5)):
+        assert lib.lora_moe_plan_create(ctypes.byref(out), rows, experts, top_k) == lb.LORA_E_ARG
+    for rows, experts, top_k in ((8, 1025, 2), (8, 64, 17), ((1 << 29) + 1, 4, 2)):
+        assert lib.lora_moe_plan_create(ctypes.byref(out), rows, experts, top_k) == lb.LORA_E_UNSUPPORTED
+    assert lib.lora_moe_route(None, P, P, None, None, P, 8, BF, 4, 0, 1, 1.0, None) == lb.LORA_E_ARG
+    assert lib.lora_moe_group(None, P, 4, None, None, None) == lb.LORA_E_ARG
+    assert lib.lora_moe_combine(None, P, 64, P, 64, P, None, 0, BF, 64, None) == lb.LORA_E_ARG
