@@ -489,6 +489,35 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
                            lora_mx_format format, int64_t n_rows, void *stream);
 
 /*
+ * The same product with its epilogue, before anything is rounded:
+ *
+ *      v = act(sum + bias[o]) + residual[i][o],   y = round(v),  (yq, ys) = v in e4m3 blocks
+ *
+ * in fp32, the sum as in lora_mx_linear.  y, or yq with ys, may be NULL, not
+ * both.  bias: DEVICE [d], dtype, or NULL.  residual [n_rows][ldr], dtype, or
+ * NULL; it may be y itself with the same stride.  act: relu v < 0 ? 0 : v; silu
+ * v / (1 + exp(-v)); gelu v (1 + erf(v / sqrt 2)) / 2; gelu_tanh v (1 + tanh(sqrt(2 /
+ * pi) (v + 0.044715 v^3))) / 2.  (LORA_ACT_SWIGLU is the experts' alone.)  Where
+ * adapters act on the product, they are added to y afterwards: an activation
+ * belongs behind them (lora_swiglu_mx), bias and residual do not mind.  Errors:
+ * LORA_E_ARG, LORA_E_EMPTY, LORA_E_UNSUPPORTED, LORA_E_HIP.
+ */
+typedef enum lora_act {
+    LORA_ACT_NONE = 0,
+    LORA_ACT_RELU = 1,
+    LORA_ACT_SILU = 2,
+    LORA_ACT_GELU = 3,
+    LORA_ACT_GELU_TANH = 4,
+    LORA_ACT_SWIGLU = 5
+} lora_act;
+
+lora_status lora_mx_linear_fused(const lora_mx_weight *w, void *y, int64_t ldy, void *yq,
+                                 int64_t ldyq, void *ys, int64_t ldys, lora_dtype dtype,
+                                 const void *q, int64_t ldq, const void *s, int64_t lds,
+                                 lora_mx_format format, const void *bias, lora_act act,
+                                 const void *residual, int64_t ldr, int64_t n_rows, void *stream);
+
+/*
  * Residual addition and RMS norm, with the norm in two forms from one pass:
  *
  *      h = x + residual                        (fp32; residual NULL: h = x)

@@ -16,6 +16,8 @@ from .build import LIB_PATH
 
 LORA_F32, LORA_BF16 = 0, 1
 LORA_MX_E4M3, LORA_MX_E2M1 = 0, 1
+LORA_ACT_NONE, LORA_ACT_RELU, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2, 3, 4
+LORA_ACT_SWIGLU = 5
 LORA_MOE_SOFTMAX, LORA_MOE_SIGMOID = 0, 1
 LORA_OK, LORA_E_ARG, LORA_E_RANK, LORA_E_SLOT, LORA_E_OCCUPIED, LORA_E_EMPTY = 0, 1, 2, 3, 4, 5
 LORA_E_NOMEM, LORA_E_HIP, LORA_E_BAD_IDS, LORA_E_UNSUPPORTED = 6, 7, 8, 9
@@ -37,7 +39,8 @@ EXPORTS = ("lora_stack_create", "lora_stack_destroy", "lora_load_slot", "lora_ev
            "lora_build_apply_noalloc", "lora_build_apply_plan",
            "lora_mx_quantize", "lora_mx_dequantize", "lora_mx_weight_create",
            "lora_mx_weight_destroy", "lora_mx_weight_load", "lora_mx_weight_load_packed",
-           "lora_mx_linear", "lora_rmsnorm_mx", "lora_swiglu_mx", "lora_block_norm_mx",
+           "lora_mx_linear", "lora_mx_linear_fused", "lora_rmsnorm_mx", "lora_swiglu_mx",
+           "lora_block_norm_mx",
            "lora_moe_plan_create", "lora_moe_plan_destroy", "lora_moe_route", "lora_moe_group",
            "lora_moe_combine",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_register",
@@ -111,6 +114,8 @@ def load(path: str | None = None):
             "lora_mx_weight_load": [P, P, I64, I, P],
             "lora_mx_weight_load_packed": [P, P, I64, P, I64, P],
             "lora_mx_linear": [P, P, I64, I, P, I64, P, I64, I, I64, P],
+            "lora_mx_linear_fused": [P, P, I64, P, I64, P, I64, I, P, I64, P, I64, I, P, I, P, I64,
+                                     I64, P],
             "lora_rmsnorm_mx": [P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, F, I, I64,
                                 I64, P],
             "lora_swiglu_mx": [P, I64, P, I64, P, I64, P, I64, I, I64, I64, P],
@@ -340,6 +345,15 @@ def lora_mx_linear(w, y: int, ldy: int, dtype: int, q: int, ldq: int, s: int, ld
     st = (_lib or load()).lora_mx_linear(w, y, ldy, dtype, q, ldq, s, lds, fmt, n_rows, stream)
     if st:
         _check(st, "lora_mx_linear")
+
+
+def lora_mx_linear_fused(w, y: int, ldy: int, yq: int, ldyq: int, ys: int, ldys: int, dtype: int,
+                         q: int, ldq: int, s: int, lds: int, fmt: int, bias: int, act: int,
+                         residual: int, ldr: int, n_rows: int, stream=None):
+    """y, or yq with ys, may be 0 (not wanted), and bias and residual (none)."""
+    st = (_lib or load()).lora_mx_linear_fused(w, y, ldy, yq, ldyq, ys, ldys, dtype, q, ldq, s, lds, fmt, bias, act, residual, ldr, n_rows, stream)
+    if st:
+        _check(st, "lora_mx_linear_fused")
 
 
 def lora_rmsnorm_mx(out: int, ldo: int, q: int, ldq: int, s: int, lds: int, h_out: int, ldh: int,

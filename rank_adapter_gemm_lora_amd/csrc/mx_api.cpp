@@ -8,6 +8,7 @@
 #include <new>
 
 #include "mx_checks.h"
+#include "mx_job.h"
 
 using namespace lora;
 
@@ -149,6 +150,47 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
     a.n_rows = n_rows;
     a.n_cu = w->n_cu;
     return status_of(launch_mx_linear(dt_of(dtype), format, a, stream_of(stream)));
+}
+
+lora_status lora_mx_linear_fused(const lora_mx_weight *w, void *y, int64_t ldy, void *yq,
+                                 int64_t ldyq, void *ys, int64_t ldys, lora_dtype dtype,
+                                 const void *q, int64_t ldq, const void *s, int64_t lds,
+                                 lora_mx_format format, const void *bias, lora_act act,
+                                 const void *residual, int64_t ldr, int64_t n_rows, void *stream)
+{
+    if (!w || !dtype_ok(dtype) || !format_ok(format) || act < LORA_ACT_NONE || act >= LORA_ACT_SWIGLU)
+        return LORA_E_ARG;
+    const lora_status st = check_shape(n_rows, w->w.k, kMxMaxK);
+    if (st != LORA_OK)
+        return st;
+    if ((!y && !yq) || !yq != !ys || (y && !dense_ok(y, ldy, w->w.d, n_rows)) ||
+        (yq && !blocks_ok(yq, ldyq, ys, ldys, LORA_MX_E4M3, w->w.d, n_rows)) ||
+        !blocks_ok(q, ldq, s, lds, format, w->w.k, n_rows) || (bias && !aligned16(bias)) ||
+        (residual && !dense_ok(residual, ldr, w->w.d, n_rows)) || !on_device(w->device))
+        return LORA_E_ARG;
+    if (!w->loaded)
+        return LORA_E_EMPTY;
+    if (n_rows == 0)
+        return LORA_OK;
+    MxLinearArgs a{};
+    a.w = w->w;
+    a.q = static_cast<const uint8_t *>(q);
+    a.ldq = ldq;
+    a.s = static_cast<const uint8_t *>(s);
+    a.lds = lds;
+    a.n_rows = n_rows;
+    a.n_cu = w->n_cu;
+    MxEpilogue e{};
+    e.bias = bias;
+    e.res = residual;
+    e.ldr = ldr;
+    e.y = y;
+    e.ldy = ldy;
+    e.b = blocks_of(yq, ldyq, ys, ldys);
+    e.d = w->w.d;
+    e.dtype = dt_of(dtype);
+    e.act = act;
+    return status_of(launch_mx_linear_fused(format, a, e, stream_of(stream)));
 }
 
 lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,

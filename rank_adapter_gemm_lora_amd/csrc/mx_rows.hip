@@ -52,21 +52,6 @@ __global__ __launch_bounds__(kRowThreads) void mx_quantize_kernel(MxRowArgs a)
     }
 }
 
-// g / (1 + exp(-g)) * u, in the values that fp32 operations one by one give (none of
-// 7.3 M bf16 or 2.9 M fp32 outputs differs), so that codes are those of an
-// unfused fp32 computation, also beside a border.  The quotient is g times the
-// hardware's reciprocal and one correction by what is left of g.  The reciprocal
-// of a denominator past 2^126 would be flushed, so past 2^64 it is taken of a
-// scaled one.
-__device__ __forceinline__ float mx_silu_mul(float g, float u)
-{
-    const float d = 1.f + expf(-g);
-    const float k = d > 0x1p64f ? 0x1p-64f : 1.f;
-    const float rc = __builtin_amdgcn_rcpf(d * k), q = g * rc;
-    const float left = fmaf(-(d * k), q, g);   // NaN where g or d is not finite: q stands
-    return (left == left ? fmaf(left, rc, q) : q) * k * u;
-}
-
 // silu(g) * u -> a dense row and blocks (512 x 14336 bf16: 14.0 us, 52 MB at 3.7
 // TB/s, bound by its instructions; 15.0 us with a true division.  The hardware's
 // exponential with its error carried takes 13.3 us at the same error, 3.6e-8 -
