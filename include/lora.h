@@ -645,6 +645,62 @@ lora_status lora_moe_group(lora_moe_plan *plan, const int32_t *ids, int64_t n_ro
                            int32_t *offsets, void *stream);
 
 /*
+ * The weights of n_experts experts, each of d output features and k inputs, in
+ * 4 bits as a lora_mx_weight's (d and k multiples of 8).  gated != 0: rows [0, d
+ * / 2) of a weight are gates and rows [d / 2, d) the values that they gate (the
+ * two slices of a gate/up projection; d a multiple of 16), and an expert has f =
+ * d / 2 outputs; otherwise f = d.  Starts empty; a load replaces one expert's
+ * weight in stream order.  Allocates device memory on the current HIP device;
+ * all later calls must run with that device current.  Reading changes nothing:
+ * products may overlap.  Limits as for weights.  Errors: LORA_E_ARG,
+ * LORA_E_UNSUPPORTED, LORA_E_NOMEM, LORA_E_HIP.
+ */
+typedef struct lora_mx_experts lora_mx_experts; /* owns the experts' 4-bit weights in HBM */
+
+lora_status lora_mx_experts_create(lora_mx_experts **out, int n_experts, int64_t d, int64_t k,
+                                   int gated);
+
+/* Free the weights (NULL is accepted); synchronises the device first. */
+lora_status lora_mx_experts_destroy(lora_mx_experts *x);
+
+/* Load one expert, as lora_mx_weight_load (dense rows W [d][ldw]) and
+ * lora_mx_weight_load_packed (rows in e2m1 blocks) load a weight.  Errors:
+ * LORA_E_ARG, LORA_E_HIP. */
+lora_status lora_mx_experts_load(lora_mx_experts *x, int expert, const void *W, int64_t ldw,
+                                 lora_dtype dtype, void *stream);
+lora_status lora_mx_experts_load_packed(lora_mx_experts *x, int expert, const void *q, int64_t ldq,
+                                        const void *s, int64_t lds, void *stream);
+
+/*
+ * Every pair's row through its expert, in one launch over groups of any sizes.
+ * For every position p of the plan's grouped order that has an expert e:
+ *
+ *      v = act(X[row(p)] W_e^T + bias_e),   y[p] = round(v),  (yq, ys)[p] = v in e4m3 blocks
+ *
+ *   X      in blocks (q, s) of either format.  LORA_MOE_ROWS: the batch's rows
+ *          [n_rows], row(p) = pair / top_k; LORA_MOE_PAIRS: rows in grouped order
+ *          [n_rows * top_k], row(p) = p
+ *   bias   DEVICE [n_experts][d], dtype, or NULL
+ *   act    for ungated weights as in lora_mx_linear_fused; for gated ones
+ *          LORA_ACT_SWIGLU: v = g / (1 + exp(-g)) * u of the sums (with bias) g
+ *          and u, none of them rounded before
+ *   y      [n_rows * top_k][ldy], f columns; yq with ys alike; y, or yq with ys,
+ *          may be NULL, not both.  Rows of pairs without an expert are left as
+ *          they were.
+ * Sums as in lora_mx_linear; their order depends on the shapes alone.  Rows are
+ * those of the last lora_moe_route / lora_moe_group of the plan, which has the
+ * experts' number.  Errors: LORA_E_ARG, LORA_E_EMPTY (an expert was not loaded or
+ * nothing was grouped yet), LORA_E_HIP.
+ */
+typedef enum lora_moe_input { LORA_MOE_ROWS = 0, LORA_MOE_PAIRS = 1 } lora_moe_input;
+
+lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan *plan, void *y,
+                                  int64_t ldy, void *yq, int64_t ldyq, void *ys, int64_t ldys,
+                                  lora_dtype dtype, const void *q, int64_t ldq, const void *s,
+                                  int64_t lds, lora_mx_format format, lora_moe_input input,
+                                  const void *bias, lora_act act, void *stream);
+
+/*
  * Bring the pairs' results back to their rows:
  *
  *      out[i] = round(residual[i] + sum_j weights[i][j] * y[position of pair (i, j)])

@@ -23,4 +23,7 @@ from .binding import (EXPORTS, LORA_BF16, LORA_F32, LORA_MX_E2M1, LORA_MX_E4M3, 
                       LORA_ACT_NONE, LORA_ACT_RELU, LORA_ACT_SILU, LORA_ACT_GELU,
                       LORA_ACT_GELU_TANH, LORA_ACT_SWIGLU, lora_mx_linear_fused,
                       LORA_MOE_SIGMOID, LORA_MOE_SOFTMAX, lora_moe_plan_create,
-                      lora_moe_plan_destroy, lora_moe_route, lora_moe_group, lora_moe_combine)
+                      lora_moe_plan_destroy, lora_moe_route, lora_moe_group, lora_moe_combine,
+                      LORA_MOE_PAIRS, LORA_MOE_ROWS, lora_mx_experts_create,
+                      lora_mx_experts_destroy, lora_mx_experts_load,
+                      lora_mx_experts_load_packed, lora_mx_expert_linear)

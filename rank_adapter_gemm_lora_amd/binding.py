@@ -19,6 +19,7 @@ LORA_MX_E4M3, LORA_MX_E2M1 = 0, 1
 LORA_ACT_NONE, LORA_ACT_RELU, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = 0, 1, 2, 3, 4
 LORA_ACT_SWIGLU = 5
 LORA_MOE_SOFTMAX, LORA_MOE_SIGMOID = 0, 1
+LORA_MOE_ROWS, LORA_MOE_PAIRS = 0, 1
 LORA_OK, LORA_E_ARG, LORA_E_RANK, LORA_E_SLOT, LORA_E_OCCUPIED, LORA_E_EMPTY = 0, 1, 2, 3, 4, 5
 LORA_E_NOMEM, LORA_E_HIP, LORA_E_BAD_IDS, LORA_E_UNSUPPORTED = 6, 7, 8, 9
 LORA_E_CAPACITY, LORA_E_NOT_FOUND = 10, 11
@@ -42,7 +43,8 @@ EXPORTS = ("lora_stack_create", "lora_stack_destroy", "lora_load_slot", "lora_ev
            "lora_mx_linear", "lora_mx_linear_fused", "lora_rmsnorm_mx", "lora_swiglu_mx",
            "lora_block_norm_mx",
            "lora_moe_plan_create", "lora_moe_plan_destroy", "lora_moe_route", "lora_moe_group",
-           "lora_moe_combine",
+           "lora_mx_experts_create", "lora_mx_experts_destroy", "lora_mx_experts_load",
+           "lora_mx_experts_load_packed", "lora_mx_expert_linear", "lora_moe_combine",
            "lora_residency_create", "lora_residency_destroy", "lora_residency_register",
            "lora_residency_unregister", "lora_residency_map_batch", "lora_residency_slot_of",
            "lora_residency_stats",
@@ -125,6 +127,11 @@ def load(path: str | None = None):
             "lora_moe_plan_destroy": [P],
             "lora_moe_route": [P, P, P, P, P, P, I64, I, I64, I, I, F, P],
             "lora_moe_group": [P, P, I64, P, P, P],
+            "lora_mx_experts_create": [PP, I, I64, I64, I],
+            "lora_mx_experts_destroy": [P],
+            "lora_mx_experts_load": [P, I, P, I64, I, P],
+            "lora_mx_experts_load_packed": [P, I, P, I64, P, I64, P],
+            "lora_mx_expert_linear": [P, P, P, I64, P, I64, P, I64, I, P, I64, P, I64, I, I, P, I, P],
             "lora_moe_combine": [P, P, I64, P, I64, P, P, I64, I, I64, P],
             "lora_residency_create": [PP, P, I, I, I64, I, P, I, I],
             "lora_residency_destroy": [P],
@@ -408,6 +415,35 @@ def lora_moe_group(plan, ids: int, n_rows: int, order: int = 0, offsets: int = 0
     st = (_lib or load()).lora_moe_group(plan, ids, n_rows, order, offsets, stream)
     if st:
         _check(st, "lora_moe_group")
+
+
+def lora_mx_experts_create(n_experts: int, d: int, k: int, gated: bool):
+    out = ctypes.c_void_p()
+    _check(load().lora_mx_experts_create(ctypes.byref(out), int(n_experts), int(d), int(k),
+                                         1 if gated else 0), "lora_mx_experts_create")
+    return out
+
+
+def lora_mx_experts_destroy(x):
+    _check(load().lora_mx_experts_destroy(x), "lora_mx_experts_destroy")
+
+
+def lora_mx_experts_load(x, expert: int, W: int, ldw: int, dtype: int, stream=None):
+    _check(load().lora_mx_experts_load(x, expert, W, ldw, dtype, stream), "lora_mx_experts_load")
+
+
+def lora_mx_experts_load_packed(x, expert: int, q: int, ldq: int, s: int, lds: int, stream=None):
+    _check(load().lora_mx_experts_load_packed(x, expert, q, ldq, s, lds, stream),
+           "lora_mx_experts_load_packed")
+
+
+def lora_mx_expert_linear(x, plan, y: int, ldy: int, yq: int, ldyq: int, ys: int, ldys: int,
+                          dtype: int, q: int, ldq: int, s: int, lds: int, fmt: int,
+                          rows_or_pairs: int, bias: int = 0, act: int = LORA_ACT_NONE, stream=None):
+    """y, or yq with ys, may be 0 (not wanted), and bias (none)."""
+    st = (_lib or load()).lora_mx_expert_linear(x, plan, y, ldy, yq, ldyq, ys, ldys, dtype, q, ldq, s, lds, fmt, rows_or_pairs, bias, act, stream)
+    if st:
+        _check(st, "lora_mx_expert_linear")
 
 
 def lora_moe_combine(plan, out: int, ldo: int, y: int, ldy: int, weights: int, residual: int,

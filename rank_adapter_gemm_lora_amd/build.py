@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["lora_api.cpp", "seg_build.hip", "shrink.hip", "expand.hip", "decode.hip", "pool.hip",
-           "merge.hip", "residency.cpp", "mx_api.cpp", "mx_rows.hip", "mx_linear.hip", "mx_fused.hip",
+           "merge.hip", "residency.cpp", "mx_api.cpp", "mx_rows.hip", "mx_linear.hip", "mx_fused.hip", "mx_experts.hip",
            "mx_block_norm.hip", "moe_api.cpp", "moe.hip"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -116,11 +116,16 @@ hipError_t launch_block_norm_mx(int dtype, const MxBlockNormArgs &a, hipStream_t
 struct MxImage {
     uint8_t *codes;      // [chunks][tiles][64][16]
     uint8_t *scales;     // [chunks / 4, rounded up][tiles][64][4]
-    int64_t d;
+    int64_t d;           // features of the image
     int64_t k;
+    int64_t half;        // 0; or outputs of a gated weight, whose rows are the gates' and then the others'
     int tiles;
     int chunks;
 };
+// Features of a gated weight's image: 32 gates and the 32 values that they
+// gate by turns, so that a lane that has the sums of eight gates has those of
+// their values in the next pair of tiles.
+inline int64_t mx_gated_features(int64_t half) { return (half + 31) / 32 * 64; }
 // From dense rows (src: dtype) or from rows in e2m1 blocks (dtype < 0: b).
 hipError_t launch_mx_image(int dtype, const void *src, int64_t ldw, const MxBlocks &b,
                            const MxImage &w, hipStream_t s);

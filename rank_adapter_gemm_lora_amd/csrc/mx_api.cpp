@@ -193,6 +193,137 @@ lora_status lora_mx_linear_fused(const lora_mx_weight *w, void *y, int64_t ldy, 
     return status_of(launch_mx_linear_fused(format, a, e, stream_of(stream)));
 }
 
+lora_status lora_mx_experts_create(lora_mx_experts **out, int n_experts, int64_t d, int64_t k,
+                                   int gated)
+{
+    if (!out)
+        return LORA_E_ARG;
+    *out = nullptr;
+    const int unit = gated ? 16 : 8;
+    if (n_experts < 1 || d < unit || d % unit != 0 || k < 8 || k % 8 != 0)
+        return LORA_E_ARG;
+    if (n_experts > LORA_MAX_EXPERTS || d > kMxMaxD || k > kMxMaxK)
+        return LORA_E_UNSUPPORTED;
+    lora_mx_experts *x = new (std::nothrow) lora_mx_experts();
+    if (!x)
+        return LORA_E_NOMEM;
+    std::memset(x, 0, sizeof *x);
+    x->experts = n_experts;
+    x->gated = gated != 0;
+    x->rows = d;
+    x->d = gated ? d / 2 : d;
+    x->w.half = gated ? d / 2 : 0;
+    x->w.d = gated ? mx_gated_features(d / 2) : d;
+    x->w.k = k;
+    x->w.tiles = (int)((x->w.d + kMxPadRows - 1) / kMxPadRows * (kMxPadRows / 16));
+    x->w.chunks = (int)((k + kMxChunk - 1) / kMxChunk);
+    x->code_stride = (int64_t)x->w.tiles * x->w.chunks * 1024;
+    x->scale_stride = (int64_t)x->w.tiles * ((x->w.chunks + 3) / 4) * 256;
+    hipError_t e = hipGetDevice(&x->device);
+    if (e == hipSuccess)
+        e = hipDeviceGetAttribute(&x->n_cu, hipDeviceAttributeMultiprocessorCount, x->device);
+    if (e == hipSuccess)
+        e = hipMalloc(reinterpret_cast<void **>(&x->w.codes), (size_t)n_experts * x->code_stride);
+    if (e == hipSuccess)
+        e = hipMalloc(reinterpret_cast<void **>(&x->w.scales), (size_t)n_experts * x->scale_stride);
+    if (e != hipSuccess) {
+        (void)hipFree(x->w.codes);
+        delete x;
+        return status_of(e);
+    }
+    *out = x;
+    return LORA_OK;
+}
+
+lora_status lora_mx_experts_destroy(lora_mx_experts *x)
+{
+    if (!x)
+        return LORA_OK;
+    const hipError_t e = hipDeviceSynchronize();
+    (void)hipFree(x->w.codes);
+    (void)hipFree(x->w.scales);
+    delete x;
+    return status_of(e);
+}
+
+namespace {
+
+lora_status experts_load(lora_mx_experts *x, int expert, int dtype, const void *W, int64_t ldw,
+                         const MxBlocks &b, void *stream)
+{
+    if (expert < 0 || expert >= x->experts || !on_device(x->device))
+        return LORA_E_ARG;
+    MxImage w = x->w;
+    w.codes += expert * x->code_stride;
+    w.scales += expert * x->scale_stride;
+    const lora_status st = status_of(launch_mx_image(dtype, W, ldw, b, w, stream_of(stream)));
+    if (st == LORA_OK && !x->loaded[expert]) {
+        x->loaded[expert] = 1;
+        ++x->n_loaded;
+    }
+    return st;
+}
+
+}  // namespace
+
+lora_status lora_mx_experts_load(lora_mx_experts *x, int expert, const void *W, int64_t ldw,
+                                 lora_dtype dtype, void *stream)
+{
+    if (!x || !dtype_ok(dtype) || !dense_ok(W, ldw, x->w.k, x->rows))
+        return LORA_E_ARG;
+    return experts_load(x, expert, dt_of(dtype), W, ldw, MxBlocks{}, stream);
+}
+
+lora_status lora_mx_experts_load_packed(lora_mx_experts *x, int expert, const void *q, int64_t ldq,
+                                        const void *s, int64_t lds, void *stream)
+{
+    if (!x || !blocks_ok(q, ldq, s, lds, LORA_MX_E2M1, x->w.k, x->rows))
+        return LORA_E_ARG;
+    return experts_load(x, expert, -1, nullptr, 0, blocks_of(q, ldq, s, lds), stream);
+}
+
+lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan *plan, void *y,
+                                  int64_t ldy, void *yq, int64_t ldyq, void *ys, int64_t ldys,
+                                  lora_dtype dtype, const void *q, int64_t ldq, const void *s,
+                                  int64_t lds, lora_mx_format format, lora_moe_input input,
+                                  const void *bias, lora_act act, void *stream)
+{
+    if (!x || !plan || !dtype_ok(dtype) || !format_ok(format) || act < LORA_ACT_NONE ||
+        act > LORA_ACT_SWIGLU || (act == LORA_ACT_SWIGLU) != (x->gated != 0) ||
+        (input != LORA_MOE_ROWS && input != LORA_MOE_PAIRS) || plan->experts != x->experts ||
+        !on_device(x->device) || !on_device(plan->device))
+        return LORA_E_ARG;
+    if (plan->n_rows < 0 || x->n_loaded < x->experts)
+        return LORA_E_EMPTY;
+    const int64_t pairs = plan->n_rows * plan->top_k;
+    const int64_t n_in = input == LORA_MOE_ROWS ? plan->n_rows : pairs;
+    if ((!y && !yq) || !yq != !ys || (y && !dense_ok(y, ldy, x->d, pairs)) ||
+        (yq && !blocks_ok(yq, ldyq, ys, ldys, LORA_MX_E4M3, x->d, pairs)) ||
+        !blocks_ok(q, ldq, s, lds, format, x->w.k, n_in) || (bias && !aligned16(bias)))
+        return LORA_E_ARG;
+    if (pairs == 0)
+        return LORA_OK;
+    MxLinearArgs a{};
+    a.w = x->w;
+    a.q = static_cast<const uint8_t *>(q);
+    a.ldq = ldq;
+    a.s = static_cast<const uint8_t *>(s);
+    a.lds = lds;
+    a.n_cu = x->n_cu;
+    MxEpilogue e{};
+    e.bias = bias;
+    e.y = y;
+    e.ldy = ldy;
+    e.b = blocks_of(yq, ldyq, ys, ldys);
+    e.d = x->d;
+    e.dtype = dt_of(dtype);
+    e.act = act;
+    e.code_stride = x->code_stride;
+    e.scale_stride = x->scale_stride;
+    const MxGroups g{plan->l, pairs, plan->experts, input == LORA_MOE_ROWS};
+    return status_of(launch_mx_experts(format, x->gated != 0, a, e, g, stream_of(stream)));
+}
+
 lora_status lora_rmsnorm_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s, int64_t lds,
                             void *h_out, int64_t ldh, const void *x, int64_t ldx,
                             const void *residual, int64_t ldr, const void *weight, float eps,

@@ -24,6 +24,27 @@ struct MxEpilogue {
     int64_t code_stride, scale_stride;   // bytes from one expert's image to the next
 };
 
+// The batch's grouping, from which the products take their row tiles.
+struct MxGroups {
+    MoeLists l;
+    int64_t pairs;
+    int experts;
+    bool by_row;         // X is in the batch's own rows
+};
+hipError_t launch_mx_experts(int format, bool gated, const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s);
 hipError_t launch_mx_linear_fused(int format, const MxLinearArgs &a, const MxEpilogue &e, hipStream_t s);
 
 }  // namespace lora
+
+struct lora_mx_experts {
+    int device;
+    int n_cu;
+    int experts;
+    int gated;
+    int64_t rows;        // of an expert's weight: outputs, or twice as many where gated
+    int64_t d;           // outputs
+    lora::MxImage w;     // the first expert's image
+    int64_t code_stride, scale_stride;
+    int n_loaded;
+    unsigned char loaded[LORA_MAX_EXPERTS];
+};

@@ -147,6 +147,15 @@ __global__ __launch_bounds__(kRowThreads) void mx_dequantize_kernel(MxRowArgs a)
 __device__ __forceinline__ int64_t mx_image_tile(int64_t o) { return (o >> 5) * 2 + ((o >> 2) & 1); }
 __device__ __forceinline__ int mx_image_row(int64_t o) { return (int)(((o >> 3) & 3) * 4 + (o & 3)); }
 
+// The weight's row that image feature j holds; -1 where it is padding.
+__device__ __forceinline__ int64_t mx_image_source(const MxImage &w, int64_t j)
+{
+    if (w.half == 0)
+        return j < w.d ? j : -1;
+    const int64_t o = (j >> 6) * 32 + (j & 31);
+    return o < w.half ? ((j >> 5) & 1) * w.half + o : -1;
+}
+
 // Dense rows -> weight image: thread = (feature, unit of 8 k).  Runs once per
 // weight, not tuned beyond reading whole 16-byte units.
 template <int DT>
@@ -155,13 +164,13 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_dense_kernel(const void 
 {
     const int units = w.chunks * 16, groups = (w.chunks + 3) / 4;
     const int unit = blockIdx.y * kRowThreads + threadIdx.x;
-    const int64_t o = blockIdx.x;
+    const int64_t o = blockIdx.x, row = mx_image_source(w, o);
     if (unit >= units)
         return;
     Vec8<DT> v;
     v.zero();
-    if (o < w.d && (int64_t)unit * 8 < w.k)
-        v.load(src, o * ldw + unit * 8);
+    if (row >= 0 && (int64_t)unit * 8 < w.k)
+        v.load(src, row * ldw + unit * 8);
     float f[8];
     v.to_f32(f);
     const uint32_t sb = mx_block_scale<LORA_MX_E2M1>(f);
@@ -184,15 +193,15 @@ __global__ __launch_bounds__(kRowThreads) void mx_image_packed_kernel(MxBlocks b
 {
     const int blocks = w.chunks * 4, groups = (w.chunks + 3) / 4;
     const int blk = blockIdx.y * kRowThreads + threadIdx.x;
-    const int64_t o = blockIdx.x;
+    const int64_t o = blockIdx.x, row = mx_image_source(w, o);
     if (blk >= blocks)
         return;
     uint4 c = make_uint4(0, 0, 0, 0);
     uint32_t sb = 0;
     const int64_t k0 = (int64_t)blk * 32;
-    if (o < w.d && k0 < w.k) {
-        c = *reinterpret_cast<const uint4 *>(b.q + o * b.ldq + (int64_t)blk * 16);
-        sb = b.s[o * b.lds + blk];
+    if (row >= 0 && k0 < w.k) {
+        c = *reinterpret_cast<const uint4 *>(b.q + row * b.ldq + (int64_t)blk * 16);
+        sb = b.s[row * b.lds + blk];
         c.y = k0 + 8 < w.k ? c.y : 0u;
         c.z = k0 + 16 < w.k ? c.z : 0u;
         c.w = k0 + 24 < w.k ? c.w : 0u;

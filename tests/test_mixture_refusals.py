@@ -48,3 +48,18 @@ def test_plan_refuses_before_the_device():
 
 def test_fused_product_refuses_without_a_weight():
     assert lb.load().lora_mx_linear_fused(None, P, 64, None, 0, None, 0, BF, P, 128, P, 16, 0, None, 0, None, 0, 1, None) == lb.LORA_E_ARG
+
+
+def test_experts_refuse_before_the_device():
+    import ctypes
+    lib = lb.load()
+    out = ctypes.c_void_p()
+    assert lib.lora_mx_experts_destroy(None) == lb.LORA_OK
+    assert lib.lora_mx_experts_create(None, 4, 64, 64, 0) == lb.LORA_E_ARG
+    for n, d, k, gated in ((0, 64, 64, 0), (4, 12, 64, 0), (4, 0, 64, 0), (4, 64, 60, 0), (4, 64, 0, 0), (4, 72, 64, 1), (4, 8, 64, 1)):
+        assert lib.lora_mx_experts_create(ctypes.byref(out), n, d, k, gated) == lb.LORA_E_ARG
+    for n, d, k in ((1025, 64, 64), (4, (1 << 22) + 8, 64), (4, 64, (1 << 20) + 8)):
+        assert lib.lora_mx_experts_create(ctypes.byref(out), n, d, k, 0) == lb.LORA_E_UNSUPPORTED
+    assert lib.lora_mx_experts_load(None, 0, P, 64, BF, None) == lb.LORA_E_ARG
+    assert lib.lora_mx_experts_load_packed(None, 0, P, 64, P, 16, None) == lb.LORA_E_ARG
+    assert lib.lora_mx_expert_linear(None, None, P, 64, None, 0, None, 0, BF, P, 128, P, 16, 0, 0, None, 0, None) == lb.LORA_E_ARG
