@@ -706,8 +706,9 @@ lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan 
  *      out[i] = round(residual[i] + sum_j weights[i][j] * y[position of pair (i, j)])
  *
  * over the pairs that have an expert, in the order of j, in fp32, rounded once.
- *   y        [n_rows * top_k][ldy], rows in the grouped order; rows of pairs
- *            without an expert are not read
+ *   y        [n_rows * top_k][ldy] in y_dtype, rows in the grouped order; rows of
+ *            pairs without an expert are not read.  (In LORA_F32 the pairs'
+ *            results are not rounded on their way, at twice a bf16 y's traffic.)
  *   weights  DEVICE float [n_rows][top_k]
  *   residual [n_rows][ldr] or NULL (0); may be out itself with the same stride
  * d columns (a multiple of 8, at most 2^22), dense matrices as above.  Rows are
@@ -716,8 +717,9 @@ lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan 
  * LORA_E_HIP.
  */
 lora_status lora_moe_combine(const lora_moe_plan *plan, void *out, int64_t ldo, const void *y,
-                             int64_t ldy, const float *weights, const void *residual, int64_t ldr,
-                             lora_dtype dtype, int64_t d, void *stream);
+                             int64_t ldy, lora_dtype y_dtype, const float *weights,
+                             const void *residual, int64_t ldr, lora_dtype dtype, int64_t d,
+                             void *stream);
 
 /* --------------------------------------------------------------- residency */
 

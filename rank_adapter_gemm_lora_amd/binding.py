@@ -132,7 +132,7 @@ def load(path: str | None = None):
             "lora_mx_experts_load": [P, I, P, I64, I, P],
             "lora_mx_experts_load_packed": [P, I, P, I64, P, I64, P],
             "lora_mx_expert_linear": [P, P, P, I64, P, I64, P, I64, I, P, I64, P, I64, I, I, P, I, P],
-            "lora_moe_combine": [P, P, I64, P, I64, P, P, I64, I, I64, P],
+            "lora_moe_combine": [P, P, I64, P, I64, I, P, P, I64, I, I64, P],
             "lora_residency_create": [PP, P, I, I, I64, I, P, I, I],
             "lora_residency_destroy": [P],
             "lora_residency_register": [P, I64, I, F, P, P],
@@ -446,10 +446,10 @@ def lora_mx_expert_linear(x, plan, y: int, ldy: int, yq: int, ldyq: int, ys: int
         _check(st, "lora_mx_expert_linear")
 
 
-def lora_moe_combine(plan, out: int, ldo: int, y: int, ldy: int, weights: int, residual: int,
-                     ldr: int, dtype: int, d: int, stream=None):
+def lora_moe_combine(plan, out: int, ldo: int, y: int, ldy: int, y_dtype: int, weights: int,
+                     residual: int, ldr: int, dtype: int, d: int, stream=None):
     """residual may be 0 (none)."""
-    st = (_lib or load()).lora_moe_combine(plan, out, ldo, y, ldy, weights, residual, ldr, dtype, d, stream)
+    st = (_lib or load()).lora_moe_combine(plan, out, ldo, y, ldy, y_dtype, weights, residual, ldr, dtype, d, stream)
     if st:
         _check(st, "lora_moe_combine")
 

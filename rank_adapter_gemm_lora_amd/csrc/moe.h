@@ -67,6 +67,7 @@ struct MoeCombineArgs {
     int64_t ldo;
     const void *y;
     int64_t ldy;
+    int y_dtype;
     const float *weights;
     const void *res;         // or null
     int64_t ldr;

@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeRouteArgs a
 // choices' loads are issued before the first is used, eight at a time.  Bound by
 // the read of y.
 constexpr int kCombineThreads = 256;
-template <int DT>
+template <int DT, int YDT>
 __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombineArgs a, int waves_a_row, MxDiv by_waves)
 {
     const uint32_t w = blockIdx.x * (kCombineThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombine
     v.to_f32(sum);
     constexpr int kAtOnce = 8;
     for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
-        Vec8<DT> y[kAtOnce];
+        Vec8<YDT> y[kAtOnce];
         float weight[kAtOnce];
         int at[kAtOnce];
 #pragma unroll
@@ -475,10 +475,14 @@ hipError_t launch_moe_combine(int dtype, const MoeCombineArgs &a, hipStream_t s)
         b.row0 = row0;
         b.rows = rows;
         const uint32_t grid = (uint32_t)((rows * waves + kCombineThreads / 64 - 1) / (kCombineThreads / 64));
-        if (dtype == DT_F32)
-            moe_combine_kernel<DT_F32><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
+        if (dtype == DT_F32 && a.y_dtype == DT_F32)
+            moe_combine_kernel<DT_F32, DT_F32><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
+        else if (dtype == DT_F32)
+            moe_combine_kernel<DT_F32, DT_BF16><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
+        else if (a.y_dtype == DT_F32)
+            moe_combine_kernel<DT_BF16, DT_F32><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
         else
-            moe_combine_kernel<DT_BF16><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
+            moe_combine_kernel<DT_BF16, DT_BF16><<<grid, kCombineThreads, 0, s>>>(b, (int)waves, by);
     });
     return hipGetLastError();
 }

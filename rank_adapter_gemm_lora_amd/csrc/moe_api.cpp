@@ -150,10 +150,11 @@ lora_status lora_moe_group(lora_moe_plan *plan, const int32_t *ids, int64_t n_ro
 }
 
 lora_status lora_moe_combine(const lora_moe_plan *plan, void *out, int64_t ldo, const void *y,
-                             int64_t ldy, const float *weights, const void *residual, int64_t ldr,
-                             lora_dtype dtype, int64_t d, void *stream)
+                             int64_t ldy, lora_dtype y_dtype, const float *weights,
+                             const void *residual, int64_t ldr, lora_dtype dtype, int64_t d,
+                             void *stream)
 {
-    if (!plan || !dtype_ok(dtype) || !on_device(plan->device))
+    if (!plan || !dtype_ok(dtype) || !dtype_ok(y_dtype) || !on_device(plan->device))
         return LORA_E_ARG;
     if (plan->n_rows < 0)
         return LORA_E_EMPTY;
@@ -171,6 +172,7 @@ lora_status lora_moe_combine(const lora_moe_plan *plan, void *out, int64_t ldo, 
     a.ldo = ldo;
     a.y = y;
     a.ldy = ldy;
+    a.y_dtype = dt_of(y_dtype);
     a.weights = weights;
     a.res = residual;
     a.ldr = ldr;

@@ -197,11 +197,10 @@ template <int FMT, int MT, int NT> struct MxChunk {
     u32x4_t w[NT], x[MT][FMT == LORA_MX_E4M3 ? 2 : 1];
 };
 
-template <class JOB, int DT, int FMT, int MT, int NT>
-__global__ __launch_bounds__(64 * kDirectWaves, 2) void mx_linear_direct_kernel(MxLinearArgs a, MxGrid grid, JOB job)
+template <class JOB, int DT, int FMT, int MT, int NT, int NW = kDirectWaves>
+__global__ __launch_bounds__(64 * NW, 2) void mx_linear_direct_kernel(MxLinearArgs a, MxGrid grid, JOB job)
 {
     static_assert(!JOB::kFused || NT == 4 || (NT == 2 && !JOB::kGated), "blocks of 32 outputs lie in one workgroup");
-    constexpr int NW = kDirectWaves;
     constexpr int kPair = NT > 1 ? 2 : 1, kParts = MT * NT / kPair;
     __shared__ f32x4_t part[NW][MT * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

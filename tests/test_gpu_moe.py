@@ -132,35 +132,36 @@ def test_group_of_given_ids(rows, experts, top_k):
             np.testing.assert_array_equal(offsets.cpu().numpy(), np.append(want_offsets, [77, 77]))
 
 
+@pytest.mark.parametrize("ydt", (BF, F32))
 @pytest.mark.parametrize("dt", (BF, F32))
 @pytest.mark.parametrize("rows,top_k,d", [(1, 1, 8), (3, 2, 520), (70, 8, 1032), (33, 11, 512), (257, 16, 136), (5, 3, 4096)])
-def test_combine(rows, top_k, d, dt):
+def test_combine(rows, top_k, d, dt, ydt):
     experts = 20
     g = np.random.default_rng(rows + d)
     ids = g.integers(-1, experts, (rows, top_k)).astype(np.int32)
     if rows > 2:
         ids[1] = -1    # a row without experts: its residual
     _, _, place = M.group(ids, experts)
-    y, hy = dense(rand(rows, rows * top_k, d), dt, 8)
+    y, hy = dense(rand(rows, rows * top_k, d), ydt, 8)
     y[int((ids >= 0).sum()):] = float("nan")   # rows of pairs without an expert are not read
     hy = y[:, :d].double().cpu().numpy()
     w = torch.from_numpy(g.random((rows, top_k)).astype(np.float32) - 0.3).to(DEV)
     w[torch.from_numpy(ids < 0).to(DEV)] = float("nan")
     r, hr = dense(rand(rows + 1, rows, d), dt, 16)
-    note(f"combine {rows}x{d} top {top_k} dtype {dt}")
+    note(f"combine {rows}x{d} top {top_k} dtype {dt} of {ydt}")
     with Plan(rows, experts, top_k) as plan:
         t = torch.from_numpy(ids).to(DEV)
         lb.lora_moe_group(plan.at, t.data_ptr(), rows, 0, 0, stream())
         for residual in (None, hr):
             out = torch.full((rows + 1, d + 16), 7.0, dtype=TD[dt], device=DEV)
-            lb.lora_moe_combine(plan.at, out.data_ptr(), out.stride(0), y.data_ptr(), y.stride(0), w.data_ptr(),
+            lb.lora_moe_combine(plan.at, out.data_ptr(), out.stride(0), y.data_ptr(), y.stride(0), ydt, w.data_ptr(),
                                 0 if residual is None else r.data_ptr(), r.stride(0), dt, d, stream())
             got = out.double().cpu().numpy()
             want, size = M.combine(hy, place, w.double().cpu().numpy(), residual)
             bad = ~(np.abs(got[:rows, :d] - want) <= HALF[dt] * np.abs(want) + 2 * (top_k + 1) * U * size + 2.0 ** -133)
             assert not bad.any(), f"{bad.sum()} of {bad.size}"
             assert (got[rows:] == 7).all() and (got[:, d:] == 7).all()
-        lb.lora_moe_combine(plan.at, r.data_ptr(), r.stride(0), y.data_ptr(), y.stride(0), w.data_ptr(), r.data_ptr(),
+        lb.lora_moe_combine(plan.at, r.data_ptr(), r.stride(0), y.data_ptr(), y.stride(0), ydt, w.data_ptr(), r.data_ptr(),
                             r.stride(0), dt, d, stream())   # in place
         assert torch.equal(r[:, :d], out[:rows, :d])
 
@@ -174,7 +175,7 @@ def test_plan_refusals():
             with pytest.raises(lb.LoraError) as e:
                 call(*args)
             assert e.value.status == status
-        refused(lb.lora_moe_combine, plan.at, p, 64, p, 64, p, 0, 0, F32, 64, stream(), status=lb.LORA_E_EMPTY)
+        refused(lb.lora_moe_combine, plan.at, p, 64, p, 64, F32, p, 0, 0, F32, 64, stream(), status=lb.LORA_E_EMPTY)
         good = [plan.at, p, p, 0, 0, p, 6, F32, 4, SOFTMAX, True, 1.0, stream()]
         for i, v in ((1, 0), (2, 0), (5, 0), (1, p + 2), (2, p + 1), (3, p + 2), (4, p + 1), (5, p + 2), (6, 5), (6, 1 << 60),
                      (7, 2), (8, -1), (8, 9), (9, 2), (11, float("inf")), (11, float("nan"))):
@@ -184,11 +185,11 @@ def test_plan_refusals():
         refused(lb.lora_moe_group, plan.at, p + 2, 4, 0, 0, stream())
         ids = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
         lb.lora_moe_group(plan.at, ids.data_ptr(), 4, 0, 0, stream())
-        good = [plan.at, p, 64, p, 64, p, p, 64, F32, 64, stream()]
-        for i, v in ((1, 0), (1, p + 4), (2, 56), (2, 60), (3, 0), (4, 56), (5, 0), (5, p + 2), (6, p + 8), (7, 56), (8, 3), (9, 60),
-                     (9, 0)):
+        good = [plan.at, p, 64, p, 64, F32, p, p, 64, F32, 64, stream()]
+        for i, v in ((1, 0), (1, p + 4), (2, 56), (2, 60), (3, 0), (4, 56), (5, 2), (6, 0), (6, p + 2), (7, p + 8), (8, 56), (9, 3),
+                     (10, 60), (10, 0)):
             refused(lb.lora_moe_combine, *good[:i], v, *good[i + 1:])
-        refused(lb.lora_moe_combine, *good[:9], (1 << 22) + 8, stream(), status=lb.LORA_E_UNSUPPORTED)
+        refused(lb.lora_moe_combine, *good[:10], (1 << 22) + 8, stream(), status=lb.LORA_E_UNSUPPORTED)
         torch.cuda.synchronize()
 
 

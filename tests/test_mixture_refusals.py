@@ -43,7 +43,7 @@ def test_plan_refuses_before_the_device():
         assert lib.lora_moe_plan_create(ctypes.byref(out), rows, experts, top_k) == lb.LORA_E_UNSUPPORTED
     assert lib.lora_moe_route(None, P, P, None, None, P, 8, BF, 4, 0, 1, 1.0, None) == lb.LORA_E_ARG
     assert lib.lora_moe_group(None, P, 4, None, None, None) == lb.LORA_E_ARG
-    assert lib.lora_moe_combine(None, P, 64, P, 64, P, None, 0, BF, 64, None) == lb.LORA_E_ARG
+    assert lib.lora_moe_combine(None, P, 64, P, 64, BF, P, None, 0, BF, 64, None) == lb.LORA_E_ARG
 
 
 def test_fused_product_refuses_without_a_weight():
