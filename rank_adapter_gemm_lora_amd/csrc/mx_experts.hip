@@ -27,13 +27,12 @@ void tile_slabs(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, i
     });
 }
 
-template <bool GATED, int FMT, int MT, int NT>
+template <bool GATED, int FMT, int MT, int NW>
 void experts_direct(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s)
 {
     typedef MxFused<true, GATED> Job;
-    constexpr int kThreads = 64 * kDirectWaves;
-    tile_slabs<Job>(a, e, g, MT - 1, NT, kThreads, [&](const MxGrid &grid, const Job &j) {
-        mx_linear_direct_kernel<Job, 0, FMT, MT, NT><<<dim3((uint32_t)grid.rows * grid.cols), kThreads, 0, s>>>(a, grid, j);
+    tile_slabs<Job>(a, e, g, MT - 1, 4, 64 * NW, [&](const MxGrid &grid, const Job &j) {
+        mx_linear_direct_kernel<Job, 0, FMT, MT, 4, NW><<<dim3((uint32_t)grid.rows * grid.cols), 64 * NW, 0, s>>>(a, grid, j);
     });
 }
 
@@ -49,23 +48,68 @@ void experts_tiles(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g
     });
 }
 
+// How the rows fall to the experts is not known here, so the tile is chosen for
+// equal groups: `mean` rows each, of as many experts as can have any.
+//
+// Few rows an expert: the stream of their weights is what counts.  Straight into
+// registers, 16 or 32 rows, and of the wavefronts that split k as few as keep
+// the chip full, so that each has a long run of k (us; rows of batch, top 8 of
+// 64; 4096 -> 2 x 1024 gated, e4m3):
+//     rows  mean    16x64 of 8 / 4 / 2      32x64 of 8 / 4 / 2       64x128
+//     1     1        8.3   8.9  10.9         9.5   9.5  11.2          -
+//     16    2       42.8  33.2  33.6        44.2  32.8  34.9         46.2
+//     64    8       60.0  44.1  45.3        59.6  44.8  47.2         52.4
+//     128   16        -   59.9  57.0        78.9  56.1  56.0         70.9
+//     256   32        -   95.7  84.3       109.2  77.2  77.7         82.2
+//     384   48        -  120.2 103.3       136.9  91.6  92.0         84.1
+// (64 rows: 285 MB of weights at 6.5 TB/s) and with k = 1024, two groups of four
+// chunks, 1024 -> 4096:
+//     64    8         -   28.5  23.8        49.1  29.1  26.6         34.3
+//     256   32        -   61.0  42.1          -   52.3  43.6         45.7
+//     384   48        -   83.4  55.8       118.0  66.9  52.6         49.7
+//
+// Small grids (few experts): the smallest tile that leaves every CU at most
+// half a workgroup, as groups are uneven (4 experts, top 2, 4096 -> 2 x 1024):
+//     rows  mean    16x64 of 8   32x64 of 4   64x64, k in 4   64x128, k in 2   64x128
+//     32    16       7.8          8.6         12.0              -                -
+//     64    32      13.2          9.7         11.9              -                -
+//     128   64        -          14.7         12.3            17.2               -
+//     256   128       -          20.1         22.0            17.7             21.0
+//     512   256       -          30.2         32.1            26.7             24.9
+//
+// Beyond, 64x128; and from 1024 rows an expert on, in grids that stay full with
+// them, the larger tile (128x256, in 4 bits 128x128), whose unfilled tiles cost
+// more the fewer rows there are (top 8 of 64, 4096 -> 2 x 1024, 64x128 / larger):
+//     e4m3   2048 rows 217 / 266   4096 rows 403 / 428   8192 rows 765 / 752   16384 rows 1490 / 1471
+//     e2m1   1024 rows  88 /  96                         8192 rows 420 / 414
 template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s)
 {
     const int64_t cu = a.n_cu, used = g.pairs < g.experts ? g.pairs : g.experts, mean = (g.pairs + used - 1) / used;
+    const int groups = (a.w.chunks + 3) / 4;   // of four chunks, what a wavefront takes at a time
     auto grid = [&](int rows, int features) {
         return used * ((mean + rows - 1) / rows) * ((a.w.d + features - 1) / features);
     };
-    if (mean <= 16)
-        return experts_direct<GATED, FMT, 1, 4>(a, e, g, s);
-    if (mean <= 32)
-        return experts_direct<GATED, FMT, 2, 4>(a, e, g, s);
-    if (grid(64, 128) <= cu)
-        return experts_tiles<GATED, FMT, 4, 1, 1, 8, FMT == LORA_MX_E4M3 ? 4 : 2>(a, e, g, s);
+    if (mean <= 8 || (mean <= 16 && grid(16, 64) <= 4 * cu) || (mean <= 32 && groups < 4) || grid(16, 64) <= cu / 2) {
+        if (groups >= 8 && grid(16, 64) <= cu)
+            return experts_direct<GATED, FMT, 1, 8>(a, e, g, s);
+        if (groups >= 4)
+            return experts_direct<GATED, FMT, 1, 4>(a, e, g, s);
+        return experts_direct<GATED, FMT, 1, 2>(a, e, g, s);
+    }
+    if (mean <= 32 || grid(32, 64) <= cu / 2) {
+        if (groups >= 4)
+            return experts_direct<GATED, FMT, 2, 4>(a, e, g, s);
+        return experts_direct<GATED, FMT, 2, 2>(a, e, g, s);
+    }
+    if (grid(64, 64) <= cu / 2)
+        return experts_tiles<GATED, FMT, 4, 1, 1, 4, 4>(a, e, g, s);
+    if (grid(64, 128) <= cu / 2)
+        return experts_tiles<GATED, FMT, 4, 1, 1, 8, 2>(a, e, g, s);
     if constexpr (FMT == LORA_MX_E4M3) {
-        if (mean >= 256 && grid(128, 256) >= 2 * cu)
+        if (mean >= 1024 && grid(128, 256) >= 8 * cu)
             return experts_tiles<GATED, FMT, 2, 4, 2, 8, 1>(a, e, g, s);
     } else {
-        if (mean >= 256 && grid(128, 128) >= 2 * cu)
+        if (mean >= 1024 && grid(128, 128) >= 8 * cu)
             return experts_tiles<GATED, FMT, 8, 1, 1, 8, 1>(a, e, g, s);
     }
     experts_tiles<GATED, FMT, 4, 1, 1, 8, 1>(a, e, g, s);
