@@ -25,7 +25,7 @@ namespace {
 constexpr int kMaxBuckets = LORA_MAX_EXPERTS + 1;   // the last: pairs without an expert
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWaves = kPlaceThreads / 64;
-constexpr int kCountThreads = 256;
+constexpr int kCountThreads = 1024;
 
 template <int CTRL> __device__ __forceinline__ uint32_t lane_move(uint32_t v)
 {
@@ -161,7 +161,7 @@ struct PlaceLds {
     int next[kMaxBuckets];                     // where this workgroup's next pair of a bucket goes
     int step[kMaxBuckets];                     // of which the current step takes so many
     int tile0[kMoeHeights][LORA_MAX_EXPERTS + 1];
-    int waves[kPlaceWaves][kMoeHeights + 1];
+    int waves[kMoeHeights + 1][kPlaceWaves];
     uint16_t wave_count[kPlaceWaves * kMaxBuckets];   // [wavefront][experts + 1]
 };
 
@@ -169,7 +169,7 @@ struct PlaceLds {
 // workgroup's share of what everybody reads of them.
 __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), E = a.experts;
     const int count = tid < E ? l.count[tid] : 0;
     int in[kMoeHeights + 1], own[kMoeHeights + 1];
 #pragma unroll
@@ -177,13 +177,14 @@ __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
         own[i] = i == 0 ? count : (count + (1 << moe_height_shift(i - 1)) - 1) >> moe_height_shift(i - 1);
         in[i] = wave_scan(own[i]);
         if (lane == 63)
-            l.waves[wave][i] = in[i];
+            l.waves[i][wave] = in[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i <= kMoeHeights; ++i)
-        for (int w = 0; w < wave; ++w)
-            in[i] += l.waves[w][i];
+    for (int i = 0; i <= kMoeHeights; ++i) {
+        const int ahead = wave_scan(lane < kPlaceWaves ? l.waves[i][lane & (kPlaceWaves - 1)] : 0);
+        in[i] += wave > 0 ? __builtin_amdgcn_readlane(ahead, wave - 1) : 0;
+    }
     int *offsets = l.step;   // not in use yet
     if (tid < E) {
         offsets[tid] = in[0] - count;
@@ -209,21 +210,33 @@ __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
         if (tid < kMoeHeights)
             a.l.n_tiles[tid] = l.tile0[tid][E];
     }
+    // the tiles of all heights, one height after the other
+    int ends[kMoeHeights];
 #pragma unroll
-    for (int i = 0; i < kMoeHeights; ++i) {
-        const int n = l.tile0[i][E], shift = moe_height_shift(i);
-        for (int t = (int)blockIdx.x * kPlaceThreads + tid; t < n; t += (int)gridDim.x * kPlaceThreads) {
-            int lo = 0, hi = E;   // the last expert whose first tile is at most t, of those that have tiles
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (l.tile0[i][mid] <= t)
-                    lo = mid;
-                else
-                    hi = mid;
+    for (int i = 0; i < kMoeHeights; ++i)
+        ends[i] = (i > 0 ? ends[i - 1] : 0) + l.tile0[i][E];
+    for (int t = (int)blockIdx.x * kPlaceThreads + tid; t < ends[kMoeHeights - 1]; t += (int)gridDim.x * kPlaceThreads) {
+        int h = 0, at = t;
+        MoeTile *tiles = a.l.tiles[0];
+#pragma unroll
+        for (int i = 1; i < kMoeHeights; ++i) {
+            if (t >= ends[i - 1]) {
+                h = i;
+                at = t - ends[i - 1];
+                tiles = a.l.tiles[i];
             }
-            const int first = offsets[lo] + ((t - l.tile0[i][lo]) << shift);
-            a.l.tiles[i][t] = MoeTile{lo, first, min(first + (1 << shift), offsets[lo] + l.count[lo]), 0};
         }
+        const int *tile0 = l.tile0[h], shift = moe_height_shift(h);
+        int lo = 0, hi = E;   // the last expert whose first tile is at most `at`: it has tiles
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tile0[mid] <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int first = offsets[lo] + ((at - tile0[lo]) << shift);
+        tiles[at] = MoeTile{lo, first, min(first + (1 << shift), offsets[lo] + l.count[lo]), 0};
     }
     __syncthreads();   // the offsets' place is the steps' again
 }
@@ -240,9 +253,11 @@ __device__ __forceinline__ void place_pairs(const MoeRouteArgs &a, PlaceLds &l, 
         const bool in = p < end;
         int key = in ? id(p) : E;
         key = (uint32_t)key < (uint32_t)E ? key : E;
-        for (int i = tid; i < kPlaceWaves * B; i += kPlaceThreads)
-            l.wave_count[i] = 0;
-        __syncthreads();
+        if (p0 > begin) {   // the first step finds them zero
+            for (int i = tid; i < kPlaceWaves * B; i += kPlaceThreads)
+                l.wave_count[i] = 0;
+            __syncthreads();
+        }
         uint64_t same = __ballot(in);
         for (int b = 0; b < bits; ++b) {
             const uint64_t set = __ballot((key >> b) & 1);
@@ -252,13 +267,15 @@ __device__ __forceinline__ void place_pairs(const MoeRouteArgs &a, PlaceLds &l, 
         if (in && rank == 0)
             l.wave_count[wave * B + key] = (uint16_t)__popcll(same);
         __syncthreads();
-        for (int b = tid; b <= E; b += kPlaceThreads) {
-            int sum = 0;
+        for (int b = tid; b < B; b += kPlaceThreads) {
+            int sum = 0, c[kPlaceWaves];
+#pragma unroll
+            for (int w = 0; w < kPlaceWaves; ++w)
+                c[w] = l.wave_count[w * B + b];
 #pragma unroll
             for (int w = 0; w < kPlaceWaves; ++w) {
-                const int c = l.wave_count[w * B + b];
                 l.wave_count[w * B + b] = (uint16_t)sum;
-                sum += c;
+                sum += c[w];
             }
             l.step[b] = sum;
         }
@@ -271,10 +288,22 @@ __device__ __forceinline__ void place_pairs(const MoeRouteArgs &a, PlaceLds &l, 
             if (a.order)
                 a.order[at] = (int)p;
         }
-        __syncthreads();
-        for (int b = tid; b <= E; b += kPlaceThreads)
-            l.next[b] += l.step[b];
+        if (p0 + kPlaceThreads < end) {
+            __syncthreads();
+            for (int b = tid; b < B; b += kPlaceThreads)
+                l.next[b] += l.step[b];
+        }
     }
+}
+
+// Counts to zero, ahead of the first use of any.
+__device__ __forceinline__ void place_clear(PlaceLds &l, int B)
+{
+    for (int i = threadIdx.x; i < B; i += kPlaceThreads)
+        l.count[i] = l.next[i] = 0;
+    for (int i = threadIdx.x; i < kPlaceWaves * B; i += kPlaceThreads)
+        l.wave_count[i] = 0;
+    __syncthreads();
 }
 
 // One workgroup: a whole batch.
@@ -284,9 +313,7 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_small_kernel(MoeRouteArgs a
     __shared__ PlaceLds l;
     __shared__ int ids[kMoeSmallPairs];
     const int tid = threadIdx.x, E = a.experts, pairs = (int)a.n_rows * a.top_k;
-    for (int e = tid; e <= E; e += kPlaceThreads)
-        l.count[e] = l.next[e] = 0;
-    __syncthreads();
+    place_clear(l, E + 1);
     if (a.logits) {
         const int lane = tid % G;
         for (int r0 = 0; r0 < a.n_rows; r0 += kPlaceThreads / G) {
@@ -354,22 +381,27 @@ __global__ __launch_bounds__(kCountThreads) void moe_count_kernel(MoeRouteArgs a
 __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeRouteArgs a)
 {
     __shared__ PlaceLds l;
-    const int tid = threadIdx.x, E = a.experts, B = E + 1;
-    for (int e = tid; e <= E; e += kPlaceThreads)
-        l.count[e] = l.next[e] = 0;
-    __syncthreads();
+    const int tid = threadIdx.x, B = a.experts + 1;
+    place_clear(l, B);
     // a bucket a thread, as often as the workgroup has room; each takes every
-    // `per`-th chunk
+    // `per`-th chunk, kAtOnce loads in flight
+    constexpr int kAtOnce = 16;
     const int per = max(1, kPlaceThreads / B);
     for (int b0 = 0; b0 < B; b0 += kPlaceThreads) {
         const int b = per > 1 ? tid % B : b0 + tid, first = per > 1 ? tid / B : 0;
         if (b < B && first < per) {
             int all = 0, ahead = 0;
-#pragma unroll 16
-            for (int c = first; c < a.n_chunks; c += per) {
-                const int n = a.hist[(int64_t)c * B + b];
-                all += n;
-                ahead += c < (int)blockIdx.x ? n : 0;
+            for (int c0 = first; c0 < a.n_chunks; c0 += per * kAtOnce) {
+                int n[kAtOnce];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    n[j] = a.hist[(int64_t)min(c0 + j * per, a.n_chunks - 1) * B + b];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int c = c0 + j * per;
+                    all += c < a.n_chunks ? n[j] : 0;
+                    ahead += c < (int)blockIdx.x ? n[j] : 0;
+                }
             }
             atomicAdd(&l.count[b], all);
             atomicAdd(&l.next[b], ahead);

@@ -53,20 +53,22 @@ void experts_tiles(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g
 //
 // Few rows an expert: the stream of their weights is what counts.  Straight into
 // registers, 16 or 32 rows, and of the wavefronts that split k as few as keep
-// the chip full, so that each has a long run of k (us; rows of batch, top 8 of
-// 64; 4096 -> 2 x 1024 gated, e4m3):
+// the chip full, so that each has a long run of k (us, on weights past the
+// last-level cache; rows of the batch, top 8 of 64; 4096 -> 2 x 1024 gated, e4m3):
 //     rows  mean    16x64 of 8 / 4 / 2      32x64 of 8 / 4 / 2       64x128
-//     1     1        8.3   8.9  10.9         9.5   9.5  11.2          -
-//     16    2       42.8  33.2  33.6        44.2  32.8  34.9         46.2
-//     64    8       60.0  44.1  45.3        59.6  44.8  47.2         52.4
-//     128   16        -   59.9  57.0        78.9  56.1  56.0         70.9
-//     256   32        -   95.7  84.3       109.2  77.2  77.7         82.2
-//     384   48        -  120.2 103.3       136.9  91.6  92.0         84.1
-// (64 rows: 285 MB of weights at 6.5 TB/s) and with k = 1024, two groups of four
+//     1     1       10.5  11.0  12.1        10.9  10.5  11.1         20.7
+//     16    2       49.0  39.2  40.2        49.7  37.8  40.4         46.3
+//     64    8       67.8  53.1  53.9        66.5  51.9  54.5         64.5
+//     128   16      86.8  66.3  63.0        81.1  61.6  62.7         72.2
+//     256   32        -   94.9  86.8       108.7  80.2  82.9         90.3
+//     384   48        -  129.0 118.0       136.7  95.5  98.3         95.2
+// (64 rows: 285 MB of weights at 5.4 TB/s) and with k = 1024, two groups of four
 // chunks, 1024 -> 4096:
-//     64    8         -   28.5  23.8        49.1  29.1  26.6         34.3
-//     256   32        -   61.0  42.1          -   52.3  43.6         45.7
-//     384   48        -   83.4  55.8       118.0  66.9  52.6         49.7
+//     64    8         -   35.0  29.4        53.0  34.4  30.7         38.0
+//     128   16        -   48.6  38.1        70.1  43.8  39.0         45.3
+//     256   32        -   72.5  50.7        94.6  57.9  47.6         50.7
+//     384   48        -   99.5  67.4       127.9  75.7  59.3         54.1
+// (2048 -> 2 x 512, top 4, 8 rows: 16x64 of 4 6.4, 32x64 of 4 7.9).
 //
 // Small grids (few experts): the smallest tile that leaves every CU at most
 // half a workgroup, as groups are uneven (4 experts, top 2, 4096 -> 2 x 1024):
@@ -89,7 +91,7 @@ template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const Mx
     auto grid = [&](int rows, int features) {
         return used * ((mean + rows - 1) / rows) * ((a.w.d + features - 1) / features);
     };
-    if (mean <= 8 || (mean <= 16 && grid(16, 64) <= 4 * cu) || (mean <= 32 && groups < 4) || grid(16, 64) <= cu / 2) {
+    if (mean <= 8 || (mean <= 16 && (groups < 4 || grid(16, 64) <= 4 * cu)) || grid(16, 64) <= cu / 2) {
         if (groups >= 8 && grid(16, 64) <= cu)
             return experts_direct<GATED, FMT, 1, 8>(a, e, g, s);
         if (groups >= 4)
