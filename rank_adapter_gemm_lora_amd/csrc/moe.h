@@ -10,7 +10,7 @@
 
 namespace lora {
 
-constexpr int kMoeMaxChunks = 512;     // chunks of rows that the larger batches are counted in
+constexpr int kMoeMaxChunks = 256;     // chunks of rows that the larger batches are counted in: one a CU
 constexpr int kMoeSmallPairs = 2048;   // batches of at most so many pairs: one workgroup, one launch
 constexpr int64_t kMoeMaxPairs = (int64_t)1 << 30;
 
@@ -27,7 +27,6 @@ struct alignas(16) MoeTile {
 // their own order inside a group, those without an expert last.
 struct MoeLists {
     int32_t *order;                 // [pairs] pair at a position
-    int32_t *row;                   // [pairs] its row
     int32_t *place;                 // [pairs] position of a pair, -1 without an expert
     int32_t *offsets;               // [experts + 1] first position of a group; the last: pairs with an expert
     int32_t *n_tiles;               // [kMoeHeights]
@@ -55,10 +54,9 @@ struct MoeRouteArgs {
     int32_t *order;          // caller's copies, or null
     int32_t *offsets;
     MoeLists l;
-    int32_t *hist;           // [chunks][experts + 1]
+    int32_t *hist;           // [chunks + 1][experts + 1]
     int64_t chunk_rows;
     int n_chunks;
-    MxDiv by_top_k;
 };
 hipError_t launch_moe_route(int dtype, const MoeRouteArgs &a, hipStream_t s);
 

@@ -12,9 +12,9 @@
 // Grouping.  A stable counting sort, as for adapters: positions of equal keys
 // inside a wavefront by ballots over the key's bits, wavefronts and steps by
 // counts in LDS.  Batches of at most kMoeSmallPairs pairs take one workgroup
-// and one launch, others two: rows in chunks, each with its histogram; then
-// every workgroup sums the histograms of all chunks (and of those ahead of its
-// own) and places its chunk.
+// and one launch (64 rows of 64 experts, top 8: 8 us, a chain of dependent
+// steps); others three: rows in chunks, each with its histogram; the
+// histograms' sums over the chunks ahead; the chunks' pairs to their places.
 #include "mx_device.h"
 #include "moe.h"
 
@@ -23,9 +23,11 @@ namespace lora {
 namespace {
 
 constexpr int kMaxBuckets = LORA_MAX_EXPERTS + 1;   // the last: pairs without an expert
-constexpr int kPlaceThreads = 1024;
-constexpr int kPlaceWaves = kPlaceThreads / 64;
-constexpr int kCountThreads = 1024;
+constexpr int kSmallThreads = 1024, kSmallSteps = kMoeSmallPairs / kSmallThreads;
+constexpr int kCountThreads = 1024;                      // at most
+constexpr int kScanBuckets = 16, kScanThreads = 256;     // of one workgroup of the sums over chunks
+constexpr int kScanChunks = kMoeMaxChunks / (kScanThreads / kScanBuckets);   // of one thread
+constexpr int kPlaceThreads = 256, kPlaceSteps = 8;
 
 template <int CTRL> __device__ __forceinline__ uint32_t lane_move(uint32_t v)
 {
@@ -56,92 +58,131 @@ template <int G> __device__ __forceinline__ float lanes_sum(float v)
 
 // A logit as an integer that orders like it; 0, below every other, for -inf and
 // NaN (experts that are switched off).  Both zeros are one.
-__device__ __forceinline__ uint32_t logit_key(float x)
+__device__ __forceinline__ uint32_t logit_key(uint32_t bits)
 {
-    const uint32_t b = __float_as_uint(x + 0.f);
-    const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return x > -INFINITY ? k : 0u;
+    constexpr int kOff = 0x007;   // the classes NaN (two) and -inf
+    const float x = __uint_as_float(bits);
+    const uint32_t b = __float_as_uint(x + 0.f), k = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+    return __builtin_amdgcn_classf(x, kOff) ? 0u : k;
 }
-__device__ __forceinline__ float logit_of(uint32_t key)
+// The same of a bf16 logit, with the expert's number in the lower half, so that
+// no two keys of a row are equal and the lower of two numbers orders higher.
+__device__ __forceinline__ uint32_t logit_key(uint32_t bits, int e)
 {
+    constexpr int kOff = 0x007;
+    const float x = __uint_as_float(bits);
+    const uint32_t b = __float_as_uint(x + 0.f), k = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+    return __builtin_amdgcn_classf(x, kOff) ? 0u : (k & 0xffff0000u) | (0xffffu - e);
+}
+template <int DT> __device__ __forceinline__ float logit_of(uint32_t key)
+{
+    if (DT == DT_BF16)   // the lower half of a negative bf16's key is all ones
+        key = key & 0x80000000u ? key & 0xffff0000u : key | 0xffffu;
     return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// Choices of one row; lane j of the row's G lanes gets choice j (id -1, weight
-// 0 where fewer experts are left).  `in`: the row exists; the lanes of one that
-// does not go through the same steps.
-template <int DT, int G, int V>
-__device__ __forceinline__ void route_row(const MoeRouteArgs &a, int64_t row, bool in, int lane, int &id, float &weight)
+// Largest first, by Batcher's merges of odd and even places (V a power of two).
+template <int V> __device__ __forceinline__ void sort_down(uint32_t (&key)[V])
 {
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t x = key[i + j], y = key[i + j + k];
+                        key[i + j] = max(x, y);
+                        key[i + j + k] = min(x, y);
+                    }
+}
+
+// Choices of one row; lane j of the row's G lanes gets choice j (id -1, weight
+// 0 where fewer experts are left).  A row past the last is the last once more.
+// FULL: there are G * V experts.
+template <int DT, int G, int V, bool FULL>
+__device__ __forceinline__ void route_row(const MoeRouteArgs &a, int row, int lane, int &id, float &weight)
+{
+    // all loads without a branch, from addresses inside the row
+    constexpr int kSize = DT == DT_F32 ? 4 : 2;
+    const char *at = static_cast<const char *>(a.logits) + min((int64_t)row, a.n_rows - 1) * a.ldl * kSize;
     uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * G + lane;
-        float x = -INFINITY;
-        if (in && e < a.experts) {
-            if constexpr (DT == DT_F32)
-                x = static_cast<const float *>(a.logits)[row * a.ldl + e];
-            else
-                x = __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.logits)[row * a.ldl + e] << 16);
-        }
-        key[v] = logit_key(x);
-        if constexpr (DT == DT_BF16)
-            key[v] = key[v] ? (key[v] & 0xffff0000u) | (0xffffu - e) : 0u;
+        const int e = FULL ? v * G + lane : min(v * G + lane, a.experts - 1);
+        if constexpr (DT == DT_F32)
+            key[v] = *reinterpret_cast<const uint32_t *>(at + (uint32_t)(e * kSize));
+        else
+            key[v] = *reinterpret_cast<const uint16_t *>(at + (uint32_t)(e * kSize));
     }
-    auto value = [](uint32_t k) {
-        // the lower half of a negative bf16's key is all ones
-        return logit_of(DT == DT_BF16 ? (k & 0x80000000u ? k & 0xffff0000u : k | 0xffffu) : k);
-    };
-    float top = 0.f, all = 0.f, mine = 0.f;
-    id = -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = v * G + lane;
+        key[v] = DT == DT_F32 ? logit_key(key[v]) : logit_key(key[v] << 16, e);
+        if (!FULL)
+            key[v] &= e < a.experts ? 0xffffffffu : 0u;
+    }
+    if constexpr (DT == DT_BF16)
+        sort_down(key);   // each lane's largest is then its first
+    float top = 0.f, all = 0.f;
+    uint32_t mine = 0;
+    int which = 0;
     for (int j = 0; j < a.top_k; ++j) {
         uint32_t m = key[0];
+        if constexpr (DT == DT_F32) {
 #pragma unroll
-        for (int v = 1; v < V; ++v)
-            m = max(m, key[v]);
+            for (int v = 1; v < V; ++v)
+                m = max(m, key[v]);
+        }
         m = lanes_reduce<G>(m, [](uint32_t p, uint32_t q) { return max(p, q); });
         if (j == 0) {
-            top = m ? value(m) : 0.f;
+            top = m ? logit_of<DT>(m) : 0.f;
             if (a.score == LORA_MOE_SOFTMAX && !a.renorm) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    all += key[v] == 0u ? 0.f : value(key[v]) == top ? 1.f : expf(value(key[v]) - top);
+                for (int v = 0; v < V; ++v) {
+                    const float x = logit_of<DT>(key[v]);
+                    all += key[v] == 0u ? 0.f : x == top ? 1.f : expf(x - top);
+                }
                 all = lanes_sum<G>(all);
             }
         }
-        int e;
         if constexpr (DT == DT_BF16) {
-            e = 0xffff - (int)(m & 0xffffu);
+            // one lane's, as keys are different, or zeros are left everywhere; by bits,
+            // as a choice of two elements would be compiled as one of their index
+            const uint32_t take = key[0] == m ? 0xffffffffu : 0u;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                key[v] = key[v] == m ? 0u : key[v];
+            for (int v = 0; v + 1 < V; ++v)
+                key[v] = (key[v + 1] & take) | (key[v] & ~take);
+            key[V - 1] &= ~take;
         } else {
             uint32_t least = 0xffffffffu;
 #pragma unroll
             for (int v = V - 1; v >= 0; --v)
                 least = key[v] == m ? (uint32_t)(v * G + lane) : least;
-            e = (int)lanes_reduce<G>(least, [](uint32_t p, uint32_t q) { return min(p, q); });
+            const int e = (int)lanes_reduce<G>(least, [](uint32_t p, uint32_t q) { return min(p, q); });
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 key[v] = v * G + lane == e ? 0u : key[v];
+            which = lane == j ? e : which;
         }
-        if (lane == j && m) {
-            id = e;
-            mine = value(m);
-        }
+        mine = lane == j ? m : mine;
     }
-    float p = 0.f;
-    if (id >= 0) {
-        if (a.score == LORA_MOE_SOFTMAX) {
-            p = mine == top ? 1.f : expf(mine - top);   // infinite logits are equal, not NaN apart
-        } else {
-            // normalised, all over e^min(top, 0): far negative logits keep their ratio
-            const float rel = a.renorm ? fminf(top, 0.f) : 0.f, low = fminf(mine, 0.f);
-            p = (low == rel ? 1.f : expf(low - rel)) / (1.f + expf(-fabsf(mine)));
-        }
+    const bool some = mine != 0;
+    id = !some ? -1 : DT == DT_F32 ? which : 0xffff - (int)(mine & 0xffffu);
+    const float x = logit_of<DT>(mine);
+    float p;
+    if (a.score == LORA_MOE_SOFTMAX) {
+        p = x == top ? 1.f : expf(x - top);   // infinite logits are equal, not NaN apart
+    } else {
+        // normalised, all over e^min(top, 0): far negative logits keep their ratio
+        const float rel = a.renorm ? fminf(top, 0.f) : 0.f, low = fminf(x, 0.f);
+        p = (low == rel ? 1.f : expf(low - rel)) / (1.f + expf(-fabsf(x)));
     }
+    p = some ? p : 0.f;
     const float sum = a.renorm ? lanes_sum<G>(p) : a.score == LORA_MOE_SOFTMAX ? all : 1.f;
-    weight = id >= 0 ? p / sum * a.scale : 0.f;
+    weight = some ? p / sum * a.scale : 0.f;
 }
 
 // Inclusive sum over a wavefront.
@@ -156,56 +197,78 @@ __device__ __forceinline__ int wave_scan(int x)
     return x;
 }
 
-struct PlaceLds {
+template <int T> struct PlaceLds {
     int count[kMaxBuckets];                    // pairs of a bucket, in the whole batch
     int next[kMaxBuckets];                     // where this workgroup's next pair of a bucket goes
     int step[kMaxBuckets];                     // of which the current step takes so many
-    int tile0[kMoeHeights][LORA_MAX_EXPERTS + 1];
-    int waves[kMoeHeights + 1][kPlaceWaves];
-    uint16_t wave_count[kPlaceWaves * kMaxBuckets];   // [wavefront][experts + 1]
+    int offsets[kMaxBuckets];
+    int tile0[kMoeHeights][kMaxBuckets];
+    int waves[kMoeHeights + 1][T / 64];
+    uint16_t wave_count[T / 64 * kMaxBuckets]; // [wavefront][experts + 1]
 };
 
 // From l.count: the groups' offsets (added to l.next) and first tiles, and this
-// workgroup's share of what everybody reads of them.
-__device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
+// workgroup's share of what the plan keeps of them.
+template <int T> __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds<T> &l)
 {
+    constexpr int kPer = (LORA_MAX_EXPERTS + T - 1) / T;   // experts of a thread, at most
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), E = a.experts;
-    const int count = tid < E ? l.count[tid] : 0;
-    int in[kMoeHeights + 1], own[kMoeHeights + 1];
+    const int per = (E + T - 1) / T;
+    int own[kPer][kMoeHeights + 1], in[kMoeHeights + 1];
+#pragma unroll
+    for (int i = 0; i <= kMoeHeights; ++i)
+        in[i] = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = tid * per + j;
+        const int n = j < per && e < E ? l.count[e] : 0;
+#pragma unroll
+        for (int i = 0; i <= kMoeHeights; ++i) {
+            own[j][i] = i == 0 ? n : (n + (1 << moe_height_shift(i - 1)) - 1) >> moe_height_shift(i - 1);
+            in[i] += own[j][i];
+        }
+    }
+    int mine[kMoeHeights + 1];
 #pragma unroll
     for (int i = 0; i <= kMoeHeights; ++i) {
-        own[i] = i == 0 ? count : (count + (1 << moe_height_shift(i - 1)) - 1) >> moe_height_shift(i - 1);
-        in[i] = wave_scan(own[i]);
+        mine[i] = in[i];
+        in[i] = wave_scan(in[i]);
         if (lane == 63)
             l.waves[i][wave] = in[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i <= kMoeHeights; ++i) {
-        const int ahead = wave_scan(lane < kPlaceWaves ? l.waves[i][lane & (kPlaceWaves - 1)] : 0);
-        in[i] += wave > 0 ? __builtin_amdgcn_readlane(ahead, wave - 1) : 0;
+        const int ahead = wave_scan(lane < T / 64 ? l.waves[i][lane % (T / 64)] : 0);
+        in[i] += (wave > 0 ? __builtin_amdgcn_readlane(ahead, wave - 1) : 0) - mine[i];
     }
-    int *offsets = l.step;   // not in use yet
-    if (tid < E) {
-        offsets[tid] = in[0] - count;
-        l.next[tid] += in[0] - count;
 #pragma unroll
-        for (int i = 0; i < kMoeHeights; ++i)
-            l.tile0[i][tid] = in[i + 1] - own[i + 1];
-        if (tid == E - 1) {
-            offsets[E] = in[0];
-            l.next[E] += in[0];
+    for (int j = 0; j < kPer; ++j) {
+        const int e = tid * per + j;
+        if (j < per && e < E) {
+            l.offsets[e] = in[0];
+            l.next[e] += in[0];
 #pragma unroll
             for (int i = 0; i < kMoeHeights; ++i)
-                l.tile0[i][E] = in[i + 1];
+                l.tile0[i][e] = in[i + 1];
+#pragma unroll
+            for (int i = 0; i <= kMoeHeights; ++i)
+                in[i] += own[j][i];
+            if (e == E - 1) {
+                l.offsets[E] = in[0];
+                l.next[E] += in[0];
+#pragma unroll
+                for (int i = 0; i < kMoeHeights; ++i)
+                    l.tile0[i][E] = in[i + 1];
+            }
         }
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-        for (int e = tid; e <= E; e += kPlaceThreads) {
-            a.l.offsets[e] = offsets[e];
+        for (int e = tid; e <= E; e += T) {
+            a.l.offsets[e] = l.offsets[e];
             if (a.offsets)
-                a.offsets[e] = offsets[e];
+                a.offsets[e] = l.offsets[e];
         }
         if (tid < kMoeHeights)
             a.l.n_tiles[tid] = l.tile0[tid][E];
@@ -215,7 +278,7 @@ __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
 #pragma unroll
     for (int i = 0; i < kMoeHeights; ++i)
         ends[i] = (i > 0 ? ends[i - 1] : 0) + l.tile0[i][E];
-    for (int t = (int)blockIdx.x * kPlaceThreads + tid; t < ends[kMoeHeights - 1]; t += (int)gridDim.x * kPlaceThreads) {
+    for (int t = (int)blockIdx.x * T + tid; t < ends[kMoeHeights - 1]; t += (int)gridDim.x * T) {
         int h = 0, at = t;
         MoeTile *tiles = a.l.tiles[0];
 #pragma unroll
@@ -235,93 +298,112 @@ __device__ __forceinline__ void place_scan(const MoeRouteArgs &a, PlaceLds &l)
             else
                 hi = mid;
         }
-        const int first = offsets[lo] + ((at - tile0[lo]) << shift);
-        tiles[at] = MoeTile{lo, first, min(first + (1 << shift), offsets[lo] + l.count[lo]), 0};
+        const int first = l.offsets[lo] + ((at - tile0[lo]) << shift);
+        tiles[at] = MoeTile{lo, first, min(first + (1 << shift), l.offsets[lo] + l.count[lo]), 0};
     }
-    __syncthreads();   // the offsets' place is the steps' again
 }
 
-// Pairs [begin, end) to their positions; id(pair): its expert, or anything
-// outside [0, experts).
-template <class F>
-__device__ __forceinline__ void place_pairs(const MoeRouteArgs &a, PlaceLds &l, int64_t begin, int64_t end, F id)
+// Pairs [begin, end) to their positions, up to T * STEPS at a time; a wavefront
+// takes neighbouring ones.  first: the ids of this thread's pairs of the first
+// time; id(pair): an id of a later one.  Anything outside [0, experts) is no
+// expert.  l.wave_count comes in zero.
+template <int T, int STEPS> __device__ __forceinline__ int place_steps(int begin, int end)
+{
+    return min(STEPS, (end - begin + T - 1) / T);
+}
+template <int T, int STEPS, class F>
+__device__ __forceinline__ void place_pairs(const MoeRouteArgs &a, PlaceLds<T> &l, int begin, int end, const int (&first)[STEPS], F id)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts;
     const int bits = 32 - __clz(E), B = E + 1;
-    for (int64_t p0 = begin; p0 < end; p0 += kPlaceThreads) {
-        const int64_t p = p0 + tid;
-        const bool in = p < end;
-        int key = in ? id(p) : E;
-        key = (uint32_t)key < (uint32_t)E ? key : E;
-        if (p0 > begin) {   // the first step finds them zero
-            for (int i = tid; i < kPlaceWaves * B; i += kPlaceThreads)
+    uint16_t *counts = l.wave_count + wave * B;
+    for (int p0 = begin; p0 < end; p0 += T * STEPS) {
+        const int steps = place_steps<T, STEPS>(p0, end);
+        const int mine = p0 + wave * 64 * steps + lane;
+        int key[STEPS], rank[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int p = mine + 64 * i;
+            key[i] = p0 == begin ? first[i] : i < steps && p < end ? id(p) : E;
+            key[i] = (uint32_t)key[i] < (uint32_t)E ? key[i] : E;
+        }
+        if (p0 > begin) {
+            for (int i = tid; i < T / 64 * B; i += T)
                 l.wave_count[i] = 0;
             __syncthreads();
         }
-        uint64_t same = __ballot(in);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((key >> b) & 1);
-            same &= (key >> b) & 1 ? set : ~set;
-        }
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        if (in && rank == 0)
-            l.wave_count[wave * B + key] = (uint16_t)__popcll(same);
-        __syncthreads();
-        for (int b = tid; b < B; b += kPlaceThreads) {
-            int sum = 0, c[kPlaceWaves];
 #pragma unroll
-            for (int w = 0; w < kPlaceWaves; ++w)
+        for (int i = 0; i < STEPS; ++i) {
+            if (i < steps) {
+                const bool in = mine + 64 * i < end;
+                uint64_t same = __ballot(in);
+                for (int b = 0; b < bits; ++b) {
+                    const uint64_t set = __ballot((key[i] >> b) & 1);
+                    same &= (key[i] >> b) & 1 ? set : ~set;
+                }
+                const int before = counts[key[i]], ahead = __popcll(same & ((1ull << lane) - 1));
+                rank[i] = before + ahead;
+                if (in && ahead == 0)
+                    counts[key[i]] = (uint16_t)(before + __popcll(same));
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+            }
+        }
+        __syncthreads();
+        for (int b = tid; b < B; b += T) {
+            int sum = 0, c[T / 64];
+#pragma unroll
+            for (int w = 0; w < T / 64; ++w)
                 c[w] = l.wave_count[w * B + b];
 #pragma unroll
-            for (int w = 0; w < kPlaceWaves; ++w) {
+            for (int w = 0; w < T / 64; ++w) {
                 l.wave_count[w * B + b] = (uint16_t)sum;
                 sum += c[w];
             }
             l.step[b] = sum;
         }
         __syncthreads();
-        if (in) {
-            const int at = l.next[key] + l.wave_count[wave * B + key] + rank;
-            a.l.order[at] = (int)p;
-            a.l.row[at] = (int)mx_div_of((uint32_t)p, a.by_top_k);
-            a.l.place[p] = key < E ? at : -1;
-            if (a.order)
-                a.order[at] = (int)p;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int p = mine + 64 * i;
+            if (i < steps && p < end) {
+                const int at = l.next[key[i]] + counts[key[i]] + rank[i];
+                a.l.order[at] = p;
+                a.l.place[p] = key[i] < E ? at : -1;
+                if (a.order)
+                    a.order[at] = p;
+            }
         }
-        if (p0 + kPlaceThreads < end) {
+        if (p0 + T * STEPS < end) {
             __syncthreads();
-            for (int b = tid; b < B; b += kPlaceThreads)
+            for (int b = tid; b < B; b += T)
                 l.next[b] += l.step[b];
         }
     }
 }
 
-// Counts to zero, ahead of the first use of any.
-__device__ __forceinline__ void place_clear(PlaceLds &l, int B)
+// One workgroup: a whole batch.
+template <int DT, int G, int V, bool FULL>
+__global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(MoeRouteArgs a)
 {
-    for (int i = threadIdx.x; i < B; i += kPlaceThreads)
+    constexpr int T = kSmallThreads;
+    __shared__ PlaceLds<T> l;
+    __shared__ int ids[kMoeSmallPairs];
+    const int tid = threadIdx.x, E = a.experts, B = E + 1, pairs = (int)a.n_rows * a.top_k;
+    for (int i = tid; i < B; i += T)
         l.count[i] = l.next[i] = 0;
-    for (int i = threadIdx.x; i < kPlaceWaves * B; i += kPlaceThreads)
+    for (int i = tid; i < T / 64 * B; i += T)
         l.wave_count[i] = 0;
     __syncthreads();
-}
-
-// One workgroup: a whole batch.
-template <int DT, int G, int V>
-__global__ __launch_bounds__(kPlaceThreads) void moe_small_kernel(MoeRouteArgs a)
-{
-    __shared__ PlaceLds l;
-    __shared__ int ids[kMoeSmallPairs];
-    const int tid = threadIdx.x, E = a.experts, pairs = (int)a.n_rows * a.top_k;
-    place_clear(l, E + 1);
     if (a.logits) {
         const int lane = tid % G;
-        for (int r0 = 0; r0 < a.n_rows; r0 += kPlaceThreads / G) {
+        for (int r0 = 0; r0 < a.n_rows; r0 += T / G) {
             const int row = r0 + tid / G;
             const bool in = row < a.n_rows;
             int id;
             float weight;
-            route_row<DT, G, V>(a, row, in, lane, id, weight);
+            route_row<DT, G, V, FULL>(a, row, lane, id, weight);
             if (in && lane < a.top_k) {
                 const int p = row * a.top_k + lane;
                 a.ids[p] = id;
@@ -331,35 +413,42 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_small_kernel(MoeRouteArgs a
             }
         }
     } else {
-        for (int p = tid; p < pairs; p += kPlaceThreads) {
+        for (int p = tid; p < pairs; p += T) {
             const int id = a.ids_in[p];
             ids[p] = id;
             atomicAdd(&l.count[(uint32_t)id < (uint32_t)E ? id : E], 1);
         }
     }
     __syncthreads();
-    place_scan(a, l);
-    place_pairs(a, l, 0, pairs, [&](int64_t p) { return ids[p]; });
+    place_scan<T>(a, l);
+    int first[kSmallSteps];
+    const int steps = place_steps<T, kSmallSteps>(0, pairs);
+#pragma unroll
+    for (int i = 0; i < kSmallSteps; ++i) {
+        const int p = (tid >> 6) * 64 * steps + (tid & 63) + 64 * i;
+        first[i] = i < steps && p < pairs ? ids[p] : E;
+    }
+    place_pairs<T, kSmallSteps>(a, l, 0, pairs, first, [&](int p) { return ids[p]; });
 }
 
 // One chunk of rows: its choices, and its histogram.
-template <int DT, int G, int V>
+template <int DT, int G, int V, bool FULL>
 __global__ __launch_bounds__(kCountThreads) void moe_count_kernel(MoeRouteArgs a)
 {
     __shared__ int hist[kMaxBuckets];
-    const int tid = threadIdx.x, E = a.experts;
-    const int64_t begin = blockIdx.x * a.chunk_rows, end = min(begin + a.chunk_rows, a.n_rows);
-    for (int e = tid; e <= E; e += kCountThreads)
+    const int tid = threadIdx.x, T = blockDim.x, E = a.experts;
+    const int begin = (int)(blockIdx.x * a.chunk_rows), end = (int)min(begin + a.chunk_rows, a.n_rows);
+    for (int e = tid; e <= E; e += T)
         hist[e] = 0;
     __syncthreads();
     if (a.logits) {
         const int lane = tid % G;
-        for (int64_t r0 = begin; r0 < end; r0 += kCountThreads / G) {
-            const int64_t row = r0 + tid / G;
+        for (int r0 = begin; r0 < end; r0 += T / G) {
+            const int row = r0 + tid / G;
             const bool in = row < end;
             int id;
             float weight;
-            route_row<DT, G, V>(a, row, in, lane, id, weight);
+            route_row<DT, G, V, FULL>(a, row, lane, id, weight);
             if (in && lane < a.top_k) {
                 a.ids[row * a.top_k + lane] = id;
                 a.weights[row * a.top_k + lane] = weight;
@@ -367,51 +456,77 @@ __global__ __launch_bounds__(kCountThreads) void moe_count_kernel(MoeRouteArgs a
             }
         }
     } else {
-        for (int64_t p = begin * a.top_k + tid; p < end * a.top_k; p += kCountThreads) {
+        for (int p = begin * a.top_k + tid; p < end * a.top_k; p += T) {
             const int id = a.ids_in[p];
             atomicAdd(&hist[(uint32_t)id < (uint32_t)E ? id : E], 1);
         }
     }
     __syncthreads();
-    for (int e = tid; e <= E; e += kCountThreads)
+    for (int e = tid; e <= E; e += T)
         a.hist[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+}
+
+// Histograms to their sums over the chunks ahead, and the batch's totals behind
+// the last chunk.  16 buckets a workgroup; 16 threads a bucket, neighbouring
+// chunks each, all of them loaded before the first is used.
+__global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(MoeRouteArgs a)
+{
+    constexpr int kParts = kScanThreads / kScanBuckets;
+    __shared__ int part[kParts][kScanBuckets];
+    const int B = a.experts + 1, in = threadIdx.x % kScanBuckets, g = threadIdx.x / kScanBuckets;
+    const int b = min((int)blockIdx.x * kScanBuckets + in, B - 1);   // past the last: its work again
+    const int per = (a.n_chunks + kParts - 1) / kParts;
+    int n[kScanChunks], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kScanChunks; ++j)
+        n[j] = a.hist[(int64_t)min(g * per + j, a.n_chunks - 1) * B + b];
+#pragma unroll
+    for (int j = 0; j < kScanChunks; ++j) {
+        n[j] = j < per && g * per + j < a.n_chunks ? n[j] : 0;
+        sum += n[j];
+    }
+    part[g][in] = sum;
+    __syncthreads();
+    int ahead = 0;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+        ahead += i < g ? part[i][in] : 0;
+    if ((int)blockIdx.x * kScanBuckets + in >= B)
+        return;
+#pragma unroll
+    for (int j = 0; j < kScanChunks; ++j) {
+        const int c = g * per + j;
+        if (j < per && c < a.n_chunks)
+            a.hist[(int64_t)c * B + b] = ahead;
+        ahead += n[j];
+    }
+    if (g == kParts - 1)
+        a.hist[(int64_t)a.n_chunks * B + b] = ahead;
 }
 
 // One chunk of rows: its pairs' positions.
 __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeRouteArgs a)
 {
-    __shared__ PlaceLds l;
+    constexpr int T = kPlaceThreads;
+    __shared__ PlaceLds<T> l;
     const int tid = threadIdx.x, B = a.experts + 1;
-    place_clear(l, B);
-    // a bucket a thread, as often as the workgroup has room; each takes every
-    // `per`-th chunk, kAtOnce loads in flight
-    constexpr int kAtOnce = 16;
-    const int per = max(1, kPlaceThreads / B);
-    for (int b0 = 0; b0 < B; b0 += kPlaceThreads) {
-        const int b = per > 1 ? tid % B : b0 + tid, first = per > 1 ? tid / B : 0;
-        if (b < B && first < per) {
-            int all = 0, ahead = 0;
-            for (int c0 = first; c0 < a.n_chunks; c0 += per * kAtOnce) {
-                int n[kAtOnce];
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
-                    n[j] = a.hist[(int64_t)min(c0 + j * per, a.n_chunks - 1) * B + b];
-#pragma unroll
-                for (int j = 0; j < kAtOnce; ++j) {
-                    const int c = c0 + j * per;
-                    all += c < a.n_chunks ? n[j] : 0;
-                    ahead += c < (int)blockIdx.x ? n[j] : 0;
-                }
-            }
-            atomicAdd(&l.count[b], all);
-            atomicAdd(&l.next[b], ahead);
-        }
-    }
-    __syncthreads();
-    place_scan(a, l);
     const int32_t *ids = a.logits ? a.ids : a.ids_in;
-    const int64_t begin = blockIdx.x * a.chunk_rows, end = min(begin + a.chunk_rows, a.n_rows);
-    place_pairs(a, l, begin * a.top_k, end * a.top_k, [&](int64_t p) { return ids[p]; });
+    const int begin = (int)(blockIdx.x * a.chunk_rows) * a.top_k;
+    const int end = (int)min((int64_t)begin + a.chunk_rows * a.top_k, a.n_rows * a.top_k);
+    const int steps = place_steps<T, kPlaceSteps>(begin, end);
+    int first[kPlaceSteps];   // on their way during the scan
+#pragma unroll
+    for (int i = 0; i < kPlaceSteps; ++i)
+        first[i] = ids[min(begin + (tid >> 6) * 64 * steps + (tid & 63) + 64 * i, end - 1)];
+    for (int b = tid; b < B; b += T) {
+        l.next[b] = a.hist[(int64_t)blockIdx.x * B + b];
+        l.count[b] = a.hist[(int64_t)a.n_chunks * B + b];
+    }
+    for (int i = tid; i < T / 64 * B; i += T)
+        l.wave_count[i] = 0;
+    __syncthreads();
+    place_scan<T>(a, l);
+    place_pairs<T, kPlaceSteps>(a, l, begin, end, first, [&](int p) { return ids[p]; });
 }
 
 // out[i] = residual[i] + sum_j weight[i][j] y[place(i, j)], summed in the
@@ -464,26 +579,41 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombine
     Vec8<DT>::store(a.out, row * a.ldo + c, sum);
 }
 
-template <int DT, int G, int V> void route_go(const MoeRouteArgs &a, hipStream_t s)
+template <int DT, int G, int V, bool FULL> void route_go(const MoeRouteArgs &a, hipStream_t s)
 {
     if (a.n_rows * a.top_k <= kMoeSmallPairs) {
-        moe_small_kernel<DT, G, V><<<1, kPlaceThreads, 0, s>>>(a);
+        moe_small_kernel<DT, G, V, FULL><<<1, kSmallThreads, 0, s>>>(a);
         return;
     }
-    moe_count_kernel<DT, G, V><<<a.n_chunks, kCountThreads, 0, s>>>(a);
+    // a chunk's rows in as few passes as a workgroup can, of equal sizes
+    const int64_t at_once = kCountThreads / G, passes = (a.chunk_rows + at_once - 1) / at_once;
+    const int64_t threads = ((a.chunk_rows + passes - 1) / passes * G + 63) / 64 * 64;
+    moe_count_kernel<DT, G, V, FULL><<<a.n_chunks, (uint32_t)threads, 0, s>>>(a);
+    moe_scan_kernel<<<(a.experts + kScanBuckets) / kScanBuckets, kScanThreads, 0, s>>>(a);
     moe_place_kernel<<<a.n_chunks, kPlaceThreads, 0, s>>>(a);
 }
 
+// 16 lanes a row up to 256 experts, 64 beyond; without the bounds of a last,
+// shorter set of experts where there is none.
+template <int DT, int G, int V> void route_full(const MoeRouteArgs &a, hipStream_t s)
+{
+    if (a.experts == G * V)
+        route_go<DT, G, V, true>(a, s);
+    else
+        route_go<DT, G, V, false>(a, s);
+}
 template <int DT> void route_pick(const MoeRouteArgs &a, hipStream_t s)
 {
-    if (!a.logits || a.experts <= 64)
-        route_go<DT, 16, 4>(a, s);
+    if (!a.logits)
+        route_go<DT, 16, 4, false>(a, s);
+    else if (a.experts <= 64)
+        route_full<DT, 16, 4>(a, s);
     else if (a.experts <= 128)
-        route_go<DT, 16, 8>(a, s);
+        route_full<DT, 16, 8>(a, s);
     else if (a.experts <= 256)
-        route_go<DT, 16, 16>(a, s);
+        route_full<DT, 16, 16>(a, s);
     else
-        route_go<DT, 64, 16>(a, s);
+        route_full<DT, 64, 16>(a, s);
 }
 
 }  // namespace

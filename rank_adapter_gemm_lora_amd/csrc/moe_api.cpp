@@ -14,16 +14,11 @@ using namespace lora;
 
 namespace {
 
-// Rows of a chunk and their number: at most 1024 pairs each (one step of the
-// placement), or more where that would make more than kMoeMaxChunks (a workgroup
-// reads all chunks' histograms).
-int64_t least_chunk(int top_k) { return 1024 / top_k / 16 * 16; }
-void chunks_of(int64_t n_rows, int top_k, int64_t &rows, int &n)
+// Rows of a chunk and their number: at most kMoeMaxChunks, of whole 16 rows.
+void chunks_of(int64_t n_rows, int64_t &rows, int &n)
 {
-    rows = least_chunk(top_k);
-    if ((n_rows + rows - 1) / rows > kMoeMaxChunks)
-        rows = ((n_rows + kMoeMaxChunks - 1) / kMoeMaxChunks + 15) / 16 * 16;
-    n = (int)((n_rows + rows - 1) / rows);
+    rows = ((n_rows + kMoeMaxChunks - 1) / kMoeMaxChunks + 15) / 16 * 16;
+    n = rows > 0 ? (int)((n_rows + rows - 1) / rows) : 0;
 }
 
 lora_status group(lora_moe_plan *plan, int dtype, MoeRouteArgs a, void *stream)
@@ -32,8 +27,7 @@ lora_status group(lora_moe_plan *plan, int dtype, MoeRouteArgs a, void *stream)
     a.top_k = plan->top_k;
     a.l = plan->l;
     a.hist = plan->hist;
-    a.by_top_k = mx_div((uint32_t)plan->top_k);
-    chunks_of(a.n_rows, a.top_k, a.chunk_rows, a.n_chunks);
+    chunks_of(a.n_rows, a.chunk_rows, a.n_chunks);
     const lora_status st = status_of(launch_moe_route(dtype, a, stream_of(stream)));
     if (st == LORA_OK)
         plan->n_rows = a.n_rows;
@@ -69,13 +63,13 @@ lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_ex
         bytes += (n + 15) / 16 * 16;
         return at;
     };
-    const int64_t order = part(pairs * 4), row = part(pairs * 4), place = part(pairs * 4);
+    const int64_t order = part(pairs * 4), place = part(pairs * 4);
     const int64_t offsets = part((n_experts + 1) * 4), n_tiles = part(kMoeHeights * 4);
     int64_t tiles[kMoeHeights];
     for (int i = 0; i < kMoeHeights; ++i)
         tiles[i] = part(moe_tile_bound(pairs, n_experts, moe_height_shift(i)) * (int64_t)sizeof(MoeTile));
-    const int64_t most = (max_rows + least_chunk(top_k) - 1) / least_chunk(top_k);
-    const int64_t hist = part((most < kMoeMaxChunks ? most : kMoeMaxChunks) * (n_experts + 1) * 4);
+    const int64_t chunks = (max_rows + 15) / 16 < kMoeMaxChunks ? (max_rows + 15) / 16 : kMoeMaxChunks;
+    const int64_t hist = part((chunks + 1) * (n_experts + 1) * 4);
     hipError_t e = hipGetDevice(&p->device);
     if (e == hipSuccess)
         e = hipMalloc(&p->memory, (size_t)bytes);
@@ -85,7 +79,6 @@ lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_ex
     }
     char *m = static_cast<char *>(p->memory);
     p->l.order = reinterpret_cast<int32_t *>(m + order);
-    p->l.row = reinterpret_cast<int32_t *>(m + row);
     p->l.place = reinterpret_cast<int32_t *>(m + place);
     p->l.offsets = reinterpret_cast<int32_t *>(m + offsets);
     p->l.n_tiles = reinterpret_cast<int32_t *>(m + n_tiles);

@@ -320,7 +320,7 @@ lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan 
     e.act = act;
     e.code_stride = x->code_stride;
     e.scale_stride = x->scale_stride;
-    const MxGroups g{plan->l, pairs, plan->experts, input == LORA_MOE_ROWS};
+    const MxGroups g{plan->l, pairs, plan->experts, plan->top_k, input == LORA_MOE_ROWS};
     return status_of(launch_mx_experts(format, x->gated != 0, a, e, g, stream_of(stream)));
 }
 

@@ -1,8 +1,8 @@
 // mx_experts.hip -- launches of the experts' products: rows grouped by expert,
 // groups of any sizes, one launch.  The kernels are those of the plain product;
 // a workgroup takes its row tile from the plan's list of tiles of its height,
-// so that a tile has rows of one expert, and the rows of X through the plan's
-// row numbers.  The grid is the most tiles that so many pairs can need; how many
+// so that a tile has rows of one expert, and the rows of X from the pairs at its
+// positions.  The grid is the most tiles that so many pairs can need; how many
 // there are is read on the device, and workgroups without a tile end at once.
 #include "mx_linear_kernels.h"
 #include "mx_slabs.h"
@@ -22,7 +22,8 @@ void tile_slabs(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, i
         j.tiles = g.l.tiles[height];
         j.n_tiles = g.l.n_tiles + height;
         j.tile0 = (int)t;
-        j.rows = g.by_row ? g.l.row : nullptr;
+        j.order = g.by_row ? g.l.order : nullptr;
+        j.by_top_k = mx_div((uint32_t)g.top_k);
         go(mx_grid((int)n, (int)cols), j);
     });
 }

@@ -20,7 +20,8 @@ struct MxEpilogue {
     const MoeTile *tiles;
     const int32_t *n_tiles;
     int tile0;               // first tile of this launch
-    const int32_t *rows;     // row of X at a position; null: X is in grouped order
+    const int32_t *order;    // pair at a position, whose row is X's; null: X is in grouped order
+    MxDiv by_top_k;
     int64_t code_stride, scale_stride;   // bytes from one expert's image to the next
 };
 
@@ -28,7 +29,7 @@ struct MxEpilogue {
 struct MxGroups {
     MoeLists l;
     int64_t pairs;
-    int experts;
+    int experts, top_k;
     bool by_row;         // X is in the batch's own rows
 };
 hipError_t launch_mx_experts(int format, bool gated, const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s);

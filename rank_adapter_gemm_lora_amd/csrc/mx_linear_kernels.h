@@ -166,7 +166,7 @@ template <class JOB> __device__ __forceinline__ uint32_t mx_source(const JOB &jo
 {
     const int at = min(r, work.end - 1);
     if constexpr (JOB::kGrouped)
-        return (uint32_t)(job.rows ? job.rows[at] : at);
+        return job.order ? mx_div_of((uint32_t)job.order[at], job.by_top_k) : (uint32_t)at;
     else
         return (uint32_t)at;
 }
