@@ -319,8 +319,11 @@ __global__ __launch_bounds__(64 * NW, 2) void mx_linear_direct_kernel(MxLinearAr
         __syncthreads();
         // unit u of a row's U: 8 outputs, four neighbouring lanes a block of 32
         constexpr int U = JOB::kGated ? NT : 2 * NT;
-        for (int i = threadIdx.x; i < 16 * MT * U; i += 64 * NW) {
-            const int r = i / U, u = i % U;
+        static_assert(64 * NW % U == 0, "a thread's unit is the same in all of its rows");
+        const int u = threadIdx.x % U;
+        MxFinish<JOB> finish(job, work.expert, tile0 * 16 / (JOB::kGated ? 2 : 1) + 8 * u);
+#pragma unroll 1
+        for (int r = threadIdx.x / U; r < 16 * MT; r += 64 * NW / U) {
             auto sums = [&](int pair, float (&f)[8]) {
                 f32x4_t v[2];
 #pragma unroll
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mx_linear_direct_kernel(MxLinearAr
             } else {
                 sums(u >> 2, f);
             }
-            mx_finish(job, work.expert, row0 + r, row0 + r < n_rows, tile0 * 16 / (JOB::kGated ? 2 : 1) + 8 * u, f, up);
+            finish.row(row0 + r, row0 + r < n_rows, f, up);
         }
         return;
     }
@@ -656,32 +659,48 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
             __syncthreads();   // everybody has read the last stage
         f32x4_t *stage = reinterpret_cast<f32x4_t *>((wv & 2) ? ((wv & 1) ? w1 : w0) : ((wv & 1) ? x1 : x0)) + (wv >> 2) * 64 * NT;
         constexpr int U = JOB::kGated ? NT : 2 * NT;   // units of a row
+        const int64_t o0 = (tile0 + wf * NT) * 16 / (JOB::kGated ? 2 : 1);
+        const int u = lane % U;
+        MxFinish<JOB> finish(job, work.expert, o0 + 8 * u);
+        // sums that are stored as they are, in fp32: 16 bytes a lane, side by side
+        const bool as_they_are = !JOB::kGated && !job.bias && job.act == LORA_ACT_NONE && (JOB::kGrouped || !job.res) &&
+                                 !job.b.q && job.dtype == DT_F32;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
+            const int first = row0 + 16 * (wr * MT + t);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 stage[m * 4 * NT + ((8 * (n / 2) + 2 * g + (n & 1)) ^ m)] = acc[t][n];
             mx_wave_fence();
-#pragma unroll 1
-            for (int i = lane; i < 16 * U; i += 64) {
-                const int r = i / U, u = i % U;
-                auto unit = [&](int c, float (&f)[8]) {
-                    const f32x4_t p = stage[r * 4 * NT + (c ^ r)], q = stage[r * 4 * NT + ((c + 1) ^ r)];
+            if (as_they_are) {
+                const int c = lane % (4 * NT);
+                float *y = static_cast<float *>(job.y) + o0 + 4 * c;
+                if (o0 + 4 * c < job.d) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] = p[e];
-                        f[4 + e] = q[e];
-                    }
-                };
-                float f[8], up[8];
-                if constexpr (JOB::kGated) {
-                    unit(16 * (u >> 2) + 2 * (u & 3), f);
-                    unit(16 * (u >> 2) + 8 + 2 * (u & 3), up);
-                } else {
-                    unit(2 * u, f);
+                    for (int r = lane / (4 * NT); r < 16; r += 16 / NT)
+                        if (first + r < n_rows)
+                            *reinterpret_cast<f32x4_t *>(y + (first + r) * job.ldy) = stage[r * 4 * NT + (c ^ r)];
                 }
-                const int row = row0 + 16 * (wr * MT + t) + r;
-                mx_finish(job, work.expert, row, row < n_rows, (tile0 + wf * NT) * 16 / (JOB::kGated ? 2 : 1) + 8 * u, f, up);
+            } else {
+#pragma unroll 1
+                for (int r = lane / U; r < 16; r += 64 / U) {
+                    auto unit = [&](int c, float (&f)[8]) {
+                        const f32x4_t p = stage[r * 4 * NT + (c ^ r)], q = stage[r * 4 * NT + ((c + 1) ^ r)];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[e] = p[e];
+                            f[4 + e] = q[e];
+                        }
+                    };
+                    float f[8], up[8];
+                    if constexpr (JOB::kGated) {
+                        unit(16 * (u >> 2) + 2 * (u & 3), f);
+                        unit(16 * (u >> 2) + 8 + 2 * (u & 3), up);
+                    } else {
+                        unit(2 * u, f);
+                    }
+                    finish.row(first + r, first + r < n_rows, f, up);
+                }
             }
             mx_wave_fence();
         }
