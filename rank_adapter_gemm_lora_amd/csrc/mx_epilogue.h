@@ -49,9 +49,34 @@ __device__ __forceinline__ float mx_logistic_mul(float v, float z)
     return v * __builtin_amdgcn_rcpf(1.f + (__builtin_amdgcn_classf(e, kPositive) ? fmaf(e, lost * kLn2, e) : e));
 }
 
-// Activations in fp32.  GELU by the complementary error function, whose value for
-// negative arguments loses nothing where 1 + erf would cancel; its tanh form
-// as v / (1 + exp(-2 z)), the same expression without the cancellation.
+// v Phi(v), Phi the normal distribution: with x = |v|, Phi(-x) = exp(-x^2 / 2) r(x),
+// r(x) = erfcx(x / sqrt 2) / 2, which falls slowly: a polynomial in 1 / (1 + 0.3 x),
+// fitted here to r on 0 <= x <= 14.5 by weighted least squares until its largest
+// relative error was least (5.8e-8).  Nothing cancels for negative v, as 1 + erf
+// would.  x^2's and its multiple's rounding are brought in behind the power of two.
+// Over all v within 8 roundings of the value (rms 1.3), in some 30 instructions
+// (512 x 4096 x 14336 with blocks 54.1 us; with the library's erfc, in branches over
+// its ranges, 56.9).
+__device__ __forceinline__ float mx_gelu(float v)
+{
+    constexpr float kC[9] = {7.37266964e-06f, 0.119484201f, 0.121945299f, 0.0945857242f, 0.142765597f,
+                             -0.0768401325f, 0.228952199f, -0.169307664f, 0.0384074338f};
+    constexpr float kHalfLog2E = 0.721347511f, kHalfLog2ELow = 9.62981517e-9f, kLn2 = 0.693147181f;
+    constexpr int kPositive = 0x180;   // finite, not zero; the others stand
+    const float x = fabsf(v), t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.f));
+    float r = kC[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+        r = fmaf(r, t, kC[i]);
+    const float s = x * x, low = fmaf(x, x, -s), a = s * -kHalfLog2E;
+    const float lost = fmaf(s, -kHalfLog2E, -a) - fmaf(low, kHalfLog2E, s * kHalfLog2ELow);
+    const float e = __builtin_amdgcn_exp2f(a);
+    const float below = r * (__builtin_amdgcn_classf(e, kPositive) ? fmaf(e, lost * kLn2, e) : e);   // Phi(-x)
+    return v * (v < 0.f ? below : 1.f - below);
+}
+
+// Activations in fp32.  The tanh form of GELU as v / (1 + exp(-2 z)), the same
+// expression without its cancellation.
 __device__ __forceinline__ void mx_activate(int act, float (&f)[8])
 {
     if (act == LORA_ACT_RELU) {
@@ -65,7 +90,7 @@ __device__ __forceinline__ void mx_activate(int act, float (&f)[8])
     } else if (act == LORA_ACT_GELU) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = 0.5f * f[e] * erfcf(f[e] * -0.70710678118654752f);
+            f[e] = mx_gelu(f[e]);
     } else if (act == LORA_ACT_GELU_TANH) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
