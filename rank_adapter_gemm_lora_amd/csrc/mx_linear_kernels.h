@@ -105,10 +105,11 @@ struct MxGrid {
     int rows, cols;
     MxDiv band;   // by 8 cols
     MxDiv last;   // by the last band's row tiles, where they are fewer than eight
+    MxDiv by_cols;
 };
 inline MxGrid mx_grid(int rows, int cols)
 {
-    return MxGrid{rows, cols, mx_div(8u * cols), mx_div(rows % 8 ? rows % 8 : 8)};
+    return MxGrid{rows, cols, mx_div(8u * cols), mx_div(rows % 8 ? rows % 8 : 8), mx_div(cols)};
 }
 struct MxPlace {
     int row, col;
@@ -145,14 +146,29 @@ struct MxWork {
     int row0, end, col, expert;
     bool none;
 };
-template <class JOB> __device__ __forceinline__ MxWork mx_work(MxLinearArgs &a, const MxGrid &grid, const JOB &job, int tile_rows)
+// BANDS: the place is taken in bands, among the tiles that there are; otherwise
+// all columns of a tile come one after the other, whatever their number, so that
+// the tile and the number are read at once (few rows: an expert's weights are
+// read by one or two tiles, and the start counts).
+template <bool BANDS, class JOB>
+__device__ __forceinline__ MxWork mx_work(MxLinearArgs &a, const MxGrid &grid, const JOB &job, int tile_rows)
 {
     if constexpr (JOB::kGrouped) {
-        const int first = job.tile0, n = min(*job.n_tiles - first, grid.rows);
-        const MxPlace at = mx_place_among(grid, max(n, 0));
-        if (at.row < 0)
-            return MxWork{0, 0, 0, 0, true};
-        const MoeTile t = job.tiles[first + at.row];
+        const int first = job.tile0;
+        MxPlace at;
+        MoeTile t;
+        if constexpr (BANDS) {
+            at = mx_place_among(grid, max(min(*job.n_tiles - first, grid.rows), 0));
+            if (at.row < 0)
+                return MxWork{0, 0, 0, 0, true};
+            t = job.tiles[first + at.row];
+        } else {
+            const int row = (int)mx_div_of(blockIdx.x, grid.by_cols);
+            at = MxPlace{row, (int)(blockIdx.x - row * grid.cols)};
+            t = job.tiles[first + row];
+            if (first + row >= *job.n_tiles)
+                return MxWork{0, 0, 0, 0, true};
+        }
         a.w.codes += t.expert * job.code_stride;
         a.w.scales += t.expert * job.scale_stride;
         return MxWork{t.first, t.end, at.col, t.expert, false};
@@ -205,7 +221,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mx_linear_direct_kernel(MxLinearAr
     __shared__ f32x4_t part[NW][MT * NT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const MxWork work = mx_work(a, grid, job, 16 * MT);
+    const MxWork work = mx_work<false>(a, grid, job, 16 * MT);
     if (work.none)
         return;
     const int n_rows = work.end, row0 = work.row0;
@@ -446,7 +462,7 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     const int set = wave / T::kSet, wv = wave % T::kSet;
     const int wr = wv / FW, wf = wv % FW;
     const int g = lane >> 4, m = lane & 15;
-    const MxWork work = mx_work(a, grid, job, T::kRows);
+    const MxWork work = mx_work<true>(a, grid, job, T::kRows);
     if (work.none)
         return;
     const int n_rows = work.end, row0 = work.row0;
