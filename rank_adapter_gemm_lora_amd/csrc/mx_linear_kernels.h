@@ -493,6 +493,10 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         ssrc[i] = n < T::kXScaleCopies ? a.s + row * a.lds : a.w.scales + tile * 256 + (lane & 15) * 16;
     }
 
+    // Groups end anywhere in a tile: a wavefront without rows only copies (512 rows
+    // top 8 of 64, 1024 -> 4096: 57 us, then 53).
+    const bool idle = JOB::kGrouped && row0 + 16 * wr * MT >= n_rows;
+
     u32x4_t sx[MT];
     uint32_t sw[NT];
     f32x4_t acc[MT][NT];
@@ -603,7 +607,8 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         // their way while the next stage's copies are issued; with one the
         // stages are short, and the copies go first.
         if constexpr (MT > 1) {
-            load(0, xc, wc);
+            if (!idle)
+                load(0, xc, wc);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (c + T::kSC < c_end)
@@ -611,6 +616,8 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
         if (st == 1 && c + 4 - T::kSC < c_end)
             fetch_scales((c - T::kSC) / 4 + 1);
         __builtin_amdgcn_sched_barrier(0);
+        if (idle)
+            return;
         if constexpr (MT == 1)
             load(0, xc, wc);
         if (c < c_end)
@@ -693,9 +700,9 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
                 float *y = static_cast<float *>(job.y) + o0 + 4 * c;
                 if (o0 + 4 * c < job.d) {
 #pragma unroll
-                    for (int r = lane / (4 * NT); r < 16; r += 16 / NT)
+                    for (int r = lane / (4 * NT); r < 16; r += 16 / NT)   // not kept in L2: 8192 rows x 8 of 1024 -> 4096 497 us, 525 if kept
                         if (first + r < n_rows)
-                            *reinterpret_cast<f32x4_t *>(y + (first + r) * job.ldy) = stage[r * 4 * NT + (c ^ r)];
+                            __builtin_nontemporal_store(stage[r * 4 * NT + (c ^ r)], reinterpret_cast<f32x4_t *>(y + (first + r) * job.ldy));
                 }
             } else {
 #pragma unroll 1
