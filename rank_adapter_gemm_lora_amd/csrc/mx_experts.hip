@@ -54,36 +54,39 @@ void experts_tiles(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g
 //
 // Few rows an expert: the stream of their weights is what counts.  Straight into
 // registers, 16 or 32 rows, and of the wavefronts that split k as few as keep
-// the chip full, so that each has a long run of k (us, on weights past the
-// last-level cache; rows of the batch, top 8 of 64; 4096 -> 2 x 1024 gated, e4m3):
-//     rows  mean    16x64 of 8 / 4 / 2      32x64 of 8 / 4 / 2       64x128
-//     1     1       10.5  11.0  12.1        10.9  10.5  11.1         20.7
-//     16    2       49.0  39.2  40.2        49.7  37.8  40.4         46.3
-//     64    8       67.8  53.1  53.9        66.5  51.9  54.5         64.5
-//     128   16      86.8  66.3  63.0        81.1  61.6  62.7         72.2
-//     256   32        -   94.9  86.8       108.7  80.2  82.9         90.3
-//     384   48        -  129.0 118.0       136.7  95.5  98.3         95.2
-// (64 rows: 285 MB of weights at 5.4 TB/s) and with k = 1024, two groups of four
-// chunks, 1024 -> 4096:
-//     64    8         -   35.0  29.4        53.0  34.4  30.7         38.0
-//     128   16        -   48.6  38.1        70.1  43.8  39.0         45.3
-//     256   32        -   72.5  50.7        94.6  57.9  47.6         50.7
-//     384   48        -   99.5  67.4       127.9  75.7  59.3         54.1
+// the chip full, so that each has a long run of k; from some 24 rows on, 64x128
+// through LDS, whose wavefronts without rows leave the matrix cores to others
+// (us, on weights past the last-level cache; rows of the batch, top 8 of 64; 4096
+// -> 2 x 1024 gated, e4m3):
+//     rows  mean    16x64 of 8 / 4 / 2      32x64 of 4 / 2       64x128
+//     1     1       10.5  11.0  12.1        10.5  11.1            20.7
+//     16    2       49.0  39.2  40.2        37.8  40.4            46.3
+//     64    8         -   51.1  49.4        46.1  49.4            48.8
+//     128   16        -   65.4  62.0        55.1  57.3            64.4
+//     192   24        -   81.3  77.1        66.4  69.8            72.4
+//     256   32        -   94.1  86.8        73.8  77.6            72.9
+//     320   40        -  111.3  99.3        86.1  87.7            78.6
+// (64 rows: 285 MB of weights at 6 TB/s; top 2 of 8, 4096 -> 2 x 14336, mean 32: 140
+// and 107); and with k = 1024, two groups of four chunks, 1024 -> 4096:
+//     64    8         -   35.2  27.5        34.5  31.9            29.2
+//     128   16        -   47.3  34.2        41.0  36.8            32.1
+//     256   32        -   72.8  50.1        56.6  45.9            38.3
 // (2048 -> 2 x 512, top 4, 8 rows: 16x64 of 4 6.4, 32x64 of 4 7.9).
 //
 // Small grids (few experts): the smallest tile that leaves every CU at most
 // half a workgroup, as groups are uneven (4 experts, top 2, 4096 -> 2 x 1024):
 //     rows  mean    16x64 of 8   32x64 of 4   64x64, k in 4   64x128, k in 2   64x128
 //     32    16       7.8          8.6         12.0              -                -
-//     64    32      13.2          9.7         11.9              -                -
-//     128   64        -          14.7         12.3            17.2               -
-//     256   128       -          20.1         22.0            17.7             21.0
-//     512   256       -          30.2         32.1            26.7             24.9
+//     64    32      13.2         10.0         12.2            17.4             20.7
+//     128   64        -          14.4         12.6            17.6             20.8
+//     256   128       -          20.4         22.0            18.1             21.2
+//     512   256       -          30.3         31.3            25.6             24.1
+// (top 2 of 8, 14336 -> 4096, mean 32: 32x64 66.7, 64x128 with k in 2 80.5).
 //
 // Beyond, 64x128; and from 1024 rows an expert on, in grids that stay full with
 // them, the larger tile (128x256, in 4 bits 128x128), whose unfilled tiles cost
 // more the fewer rows there are (top 8 of 64, 4096 -> 2 x 1024, 64x128 / larger):
-//     e4m3   2048 rows 217 / 266   4096 rows 403 / 428   8192 rows 765 / 752   16384 rows 1490 / 1471
+//     e4m3   2048 rows 217 / 266   4096 rows 386 / 399   8192 rows 749 / 728
 //     e2m1   1024 rows  88 /  96                         8192 rows 420 / 414
 template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s)
 {
@@ -92,14 +95,14 @@ template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const Mx
     auto grid = [&](int rows, int features) {
         return used * ((mean + rows - 1) / rows) * ((a.w.d + features - 1) / features);
     };
-    if (mean <= 8 || (mean <= 16 && (groups < 4 || grid(16, 64) <= 4 * cu)) || grid(16, 64) <= cu / 2) {
+    if (mean <= 8 || (mean <= 12 && groups < 4) || (mean <= 16 && grid(16, 64) <= cu) || grid(16, 64) <= cu / 2) {
         if (groups >= 8 && grid(16, 64) <= cu)
             return experts_direct<GATED, FMT, 1, 8>(a, e, g, s);
         if (groups >= 4)
             return experts_direct<GATED, FMT, 1, 4>(a, e, g, s);
         return experts_direct<GATED, FMT, 1, 2>(a, e, g, s);
     }
-    if (mean <= 32 || grid(32, 64) <= cu / 2) {
+    if ((mean <= 24 && groups >= 4) || (mean <= 32 && grid(64, 128) <= cu) || grid(32, 64) <= cu / 2) {
         if (groups >= 4)
             return experts_direct<GATED, FMT, 2, 4>(a, e, g, s);
         return experts_direct<GATED, FMT, 2, 2>(a, e, g, s);
