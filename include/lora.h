@@ -499,7 +499,8 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
  * v / (1 + exp(-v)); gelu v (1 + erf(v / sqrt 2)) / 2; gelu_tanh v (1 + tanh(sqrt(2 /
  * pi) (v + 0.044715 v^3))) / 2.  (LORA_ACT_SWIGLU is the experts' alone.)  Where
  * adapters act on the product, they are added to y afterwards: an activation
- * belongs behind them (lora_swiglu_mx), bias and residual do not mind.  Errors:
+ * belongs behind them (lora_swiglu_mx), bias and residual do not mind.  Otherwise
+ * the outputs overlap nothing that is read.  Errors:
  * LORA_E_ARG, LORA_E_EMPTY, LORA_E_UNSUPPORTED, LORA_E_HIP.
  */
 typedef enum lora_act {
@@ -599,9 +600,14 @@ typedef enum lora_moe_score { LORA_MOE_SOFTMAX = 0, LORA_MOE_SIGMOID = 1 } lora_
 /*
  * Create a plan for up to max_rows rows of top_k <= n_experts choices each.
  * Allocates device memory on the current HIP device; all later calls must run
- * with that device current.  A plan holds one grouping at a time: calls that
- * use it must not overlap with one that writes it, and a graph captured with a
- * plan belongs to the number of rows it was captured with.  Errors: LORA_E_ARG,
+ * with that device current.  A plan holds one grouping at a time, that of the
+ * last lora_moe_route / lora_moe_group to run; calls that read it must not
+ * overlap with one that writes it, and a plan must not be used from two host
+ * threads at once.  The number of rows of a call that reads it is that of the
+ * last such call made when it was made (or captured): a graph needs the grouping
+ * of as many rows as it was captured with, by capturing that too or by making it
+ * anew before the replay.  Under another grouping results are undefined, but
+ * nothing outside the buffers of so many rows is touched.  Errors: LORA_E_ARG,
  * LORA_E_UNSUPPORTED, LORA_E_NOMEM, LORA_E_HIP.
  */
 lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_experts, int top_k);
@@ -686,7 +692,7 @@ lora_status lora_mx_experts_load_packed(lora_mx_experts *x, int expert, const vo
  *          and u, none of them rounded before
  *   y      [n_rows * top_k][ldy], f columns; yq with ys alike; y, or yq with ys,
  *          may be NULL, not both.  Rows of pairs without an expert are left as
- *          they were.
+ *          they were.  The outputs overlap nothing that is read.
  * Sums as in lora_mx_linear; their order depends on the shapes alone.  Rows are
  * those of the last lora_moe_route / lora_moe_group of the plan, which has the
  * experts' number.  Errors: LORA_E_ARG, LORA_E_EMPTY (an expert was not loaded or
@@ -711,6 +717,7 @@ lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan 
  *            results are not rounded on their way, at twice a bf16 y's traffic.)
  *   weights  DEVICE float [n_rows][top_k]
  *   residual [n_rows][ldr] or NULL (0); may be out itself with the same stride
+ *            (out overlaps nothing else that is read)
  * d columns (a multiple of 8, at most 2^22), dense matrices as above.  Rows are
  * those of the last lora_moe_route / lora_moe_group of the plan.  Errors:
  * LORA_E_ARG, LORA_E_EMPTY (nothing was grouped yet), LORA_E_UNSUPPORTED,

@@ -551,6 +551,7 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombine
         v.load(a.res, row * a.ldr + c);
     v.to_f32(sum);
     constexpr int kAtOnce = 8;
+    const int64_t pairs = a.n_rows * a.top_k;
     for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
         Vec8<YDT> y[kAtOnce];
         float weight[kAtOnce];
@@ -559,6 +560,7 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombine
         for (int j = 0; j < kAtOnce; ++j) {
             const int64_t p = row * a.top_k + min(j0 + j, a.top_k - 1);
             at[j] = j0 + j < a.top_k ? a.place[p] : -1;
+            at[j] = at[j] < pairs ? at[j] : -1;   // y has no more rows, whatever grouping the plan holds by now
             weight[j] = a.weights[p];
         }
 #pragma unroll

@@ -73,7 +73,13 @@ lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_ex
     hipError_t e = hipGetDevice(&p->device);
     if (e == hipSuccess)
         e = hipMalloc(&p->memory, (size_t)bytes);
+    // no tiles, until a grouping has run
+    if (e == hipSuccess)
+        e = hipMemset(static_cast<char *>(p->memory) + n_tiles, 0, kMoeHeights * 4);
+    if (e == hipSuccess)
+        e = hipStreamSynchronize(nullptr);
     if (e != hipSuccess) {
+        (void)hipFree(p->memory);
         delete p;
         return status_of(e);
     }

@@ -24,6 +24,8 @@ void tile_slabs(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, i
         j.tile0 = (int)t;
         j.order = g.by_row ? g.l.order : nullptr;
         j.by_top_k = mx_div((uint32_t)g.top_k);
+        j.pairs = (int)g.pairs;
+        j.in_rows = (int)(g.pairs / g.top_k);
         go(mx_grid((int)n, (int)cols), j);
     });
 }

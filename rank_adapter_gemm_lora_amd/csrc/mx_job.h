@@ -22,6 +22,8 @@ struct MxEpilogue {
     int tile0;               // first tile of this launch
     const int32_t *order;    // pair at a position, whose row is X's; null: X is in grouped order
     MxDiv by_top_k;
+    int pairs, in_rows;      // rows of the outputs and of X: nothing beyond is touched,
+                             // whatever grouping the plan holds by now
     int64_t code_stride, scale_stride;   // bytes from one expert's image to the next
 };
 

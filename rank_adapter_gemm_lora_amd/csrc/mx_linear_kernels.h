@@ -171,7 +171,7 @@ __device__ __forceinline__ MxWork mx_work(MxLinearArgs &a, const MxGrid &grid, c
         }
         a.w.codes += t.expert * job.code_stride;
         a.w.scales += t.expert * job.scale_stride;
-        return MxWork{t.first, t.end, at.col, t.expert, false};
+        return MxWork{t.first, min(t.end, job.pairs), at.col, t.expert, t.first >= job.pairs};
     } else {
         const MxPlace at = mx_place(grid);
         return MxWork{at.row * tile_rows, (int)a.n_rows, at.col, 0, false};
@@ -182,7 +182,7 @@ template <class JOB> __device__ __forceinline__ uint32_t mx_source(const JOB &jo
 {
     const int at = min(r, work.end - 1);
     if constexpr (JOB::kGrouped)
-        return job.order ? mx_div_of((uint32_t)job.order[at], job.by_top_k) : (uint32_t)at;
+        return job.order ? min(mx_div_of((uint32_t)job.order[at], job.by_top_k), (uint32_t)job.in_rows - 1) : (uint32_t)at;
     else
         return (uint32_t)at;
 }

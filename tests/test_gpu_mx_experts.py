@@ -265,3 +265,47 @@ def test_experts_refusals():
         torch.cuda.synchronize()
         lb.lora_mx_experts_destroy(x)
         lb.lora_mx_experts_destroy(gated)
+
+
+@pytest.mark.parametrize("top_k,experts", [(2, 3), (1, 40)])
+def test_experts_under_a_grouping_of_more_rows(top_k, experts):
+    """A grouping that was only captured sets the number of rows, not what the plan holds: calls made then stay inside the
+    buffers of that number, though the plan's tiles and places go beyond."""
+    note(f"experts under a grouping of more rows, top {top_k} of {experts}")
+    few, many, k, f = 24, 600, 264, 136
+    g = np.random.default_rng(7)
+    packed = [R.quantize(g.standard_normal((f, k)), R.E2M1) for _ in range(experts)]
+    xq, xs = (torch.from_numpy(t).to(DEV) for t in R.quantize(rand(1, few, k, 0.3), R.E4M3))
+    ids = torch.from_numpy(g.integers(0, experts, (many, top_k)).astype(np.int32)).to(DEV)
+    y = torch.full((few * top_k + many, f), 7.0, device=DEV)
+    out = torch.full((few + many, f), 7.0, device=DEV)
+    w = torch.ones(few, top_k, device=DEV)
+    with Experts(packed, f, k, False) as x, Plan(many, experts, top_k) as plan:
+        def products():
+            lb.lora_mx_expert_linear(x.at, plan.at, y.data_ptr(), f, 0, 0, 0, 0, F32, *held(xq, xs), R.E4M3, lb.LORA_MOE_ROWS, 0,
+                                     lb.LORA_ACT_NONE, stream())
+            lb.lora_moe_combine(plan.at, out.data_ptr(), f, y.data_ptr(), f, F32, w.data_ptr(), 0, 0, F32, f, stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):   # nothing has run yet: no tiles
+            lb.lora_moe_group(plan.at, ids.data_ptr(), few, 0, 0, stream())
+        lb.lora_mx_expert_linear(x.at, plan.at, y.data_ptr(), f, 0, 0, 0, 0, F32, *held(xq, xs), R.E4M3, lb.LORA_MOE_ROWS, 0,
+                                 lb.LORA_ACT_NONE, stream())
+        torch.cuda.synchronize()
+        assert (y == 7).all()
+        lb.lora_moe_group(plan.at, ids.data_ptr(), few, 0, 0, stream())
+        products()
+        torch.cuda.synchronize()
+        want = out[:few].clone()
+        lb.lora_moe_group(plan.at, ids.data_ptr(), many, 0, 0, stream())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lb.lora_moe_group(plan.at, ids.data_ptr(), few, 0, 0, stream())
+        products()
+        torch.cuda.synchronize()
+        assert (y[few * top_k:] == 7).all() and (out[few:] == 7).all()
+        graph.replay()      # now the plan holds what the calls were made for
+        products()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:few], want)
+        assert (y[few * top_k:] == 7).all() and (out[few:] == 7).all()
