@@ -12,9 +12,12 @@
 // Grouping.  A stable counting sort, as for adapters: positions of equal keys
 // inside a wavefront by ballots over the key's bits, wavefronts and steps by
 // counts in LDS.  Batches of at most kMoeSmallPairs pairs take one workgroup
-// and one launch (64 rows of 64 experts, top 8: 8 us, a chain of dependent
+// and one launch (64 rows of 64 experts, top 8: 7.2 us, a chain of dependent
 // steps); others three: rows in chunks, each with its histogram; the
 // histograms' sums over the chunks ahead; the chunks' pairs to their places.
+// 35422 rows of 128 experts, top 8, bf16: 9.8 + 3.7 + 9.4 us, the first bound by its
+// instructions (19 us with the maximum over unsorted keys), the last by scattered
+// writes of 4 bytes (four arrays where the caller wants the order too).
 #include "mx_device.h"
 #include "moe.h"
 
@@ -533,7 +536,7 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeRouteArgs a
 // choices' order in fp32, rounded once.  A wavefront takes 64 units of 8 columns
 // of one row, so places and weights are the same in all of its lanes; all
 // choices' loads are issued before the first is used, eight at a time.  Bound by
-// the read of y.
+// the read of y: 8192 rows of 8 x 4096 fp32, 1.34 GB in 247 - 281 us (4.8 - 5.4 TB/s).
 constexpr int kCombineThreads = 256;
 template <int DT, int YDT>
 __global__ __launch_bounds__(kCombineThreads) void moe_combine_kernel(MoeCombineArgs a, int waves_a_row, MxDiv by_waves)

