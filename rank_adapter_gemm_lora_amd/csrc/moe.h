@@ -28,7 +28,6 @@ struct alignas(16) MoeTile {
 struct MoeLists {
     int32_t *order;                 // [pairs] pair at a position
     int32_t *place;                 // [pairs] position of a pair, -1 without an expert
-    int32_t *offsets;               // [experts + 1] first position of a group; the last: pairs with an expert
     int32_t *n_tiles;               // [kMoeHeights]
     MoeTile *tiles[kMoeHeights];
 };
@@ -51,8 +50,8 @@ struct MoeRouteArgs {
     int experts, top_k;
     int score, renorm;
     float scale;
-    int32_t *order;          // caller's copies, or null
-    int32_t *offsets;
+    int32_t *order;          // the caller's copy, or null
+    int32_t *offsets;        // or null: [experts + 1] first position of a group; the last: pairs with an expert
     MoeLists l;
     int32_t *hist;           // [chunks + 1][experts + 1]
     int64_t chunk_rows;

@@ -268,11 +268,9 @@ template <int T> __device__ __forceinline__ void place_scan(const MoeRouteArgs &
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-        for (int e = tid; e <= E; e += T) {
-            a.l.offsets[e] = l.offsets[e];
-            if (a.offsets)
+        if (a.offsets)
+            for (int e = tid; e <= E; e += T)
                 a.offsets[e] = l.offsets[e];
-        }
         if (tid < kMoeHeights)
             a.l.n_tiles[tid] = l.tile0[tid][E];
     }

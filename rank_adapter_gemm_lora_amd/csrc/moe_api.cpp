@@ -64,7 +64,7 @@ lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_ex
         return at;
     };
     const int64_t order = part(pairs * 4), place = part(pairs * 4);
-    const int64_t offsets = part((n_experts + 1) * 4), n_tiles = part(kMoeHeights * 4);
+    const int64_t n_tiles = part(kMoeHeights * 4);
     int64_t tiles[kMoeHeights];
     for (int i = 0; i < kMoeHeights; ++i)
         tiles[i] = part(moe_tile_bound(pairs, n_experts, moe_height_shift(i)) * (int64_t)sizeof(MoeTile));
@@ -86,7 +86,6 @@ lora_status lora_moe_plan_create(lora_moe_plan **out, int64_t max_rows, int n_ex
     char *m = static_cast<char *>(p->memory);
     p->l.order = reinterpret_cast<int32_t *>(m + order);
     p->l.place = reinterpret_cast<int32_t *>(m + place);
-    p->l.offsets = reinterpret_cast<int32_t *>(m + offsets);
     p->l.n_tiles = reinterpret_cast<int32_t *>(m + n_tiles);
     for (int i = 0; i < kMoeHeights; ++i)
         p->l.tiles[i] = reinterpret_cast<MoeTile *>(m + tiles[i]);

@@ -31,8 +31,8 @@ def route(x, top_k, score, renorm, scale):
             total = sum(p(e) for e in chosen) if renorm else 1.0
         for j, e in enumerate(chosen):
             ids[i, j], w[i, j] = e, scale * p(e) / total
-        ends = [abs(x[i, e] - top) for e in chosen if np.isfinite(x[i, e] - top)] + [abs(x[i, e]) for e in chosen if np.isfinite(x[i, e])]
-        far[i] = max(ends, default=0.0)
+        finite = [x[i, e] for e in chosen if np.isfinite(x[i, e])]
+        far[i] = max([abs(v) for v in finite] + [abs(v - top) for v in finite if np.isfinite(top)], default=0.0)
     return ids, w, far
 
 

@@ -78,7 +78,8 @@ def check_route(got, hx, K, score, renorm, scale, what):
 
 # one and several workgroups, steps that end inside a chunk, every width of the expert groups
 SHAPES = [(1, 1, 1), (1, 8, 2), (3, 5, 5), (16, 16, 16), (64, 64, 8), (129, 60, 4), (200, 128, 8), (300, 65, 7), (257, 256, 8),
-          (700, 129, 3), (130, 1000, 16), (90, 1024, 5), (3000, 33, 1), (1500, 257, 11)]
+          (700, 129, 3), (130, 1000, 16), (90, 1024, 5), (3000, 33, 1), (1500, 257, 11),
+          (400, 64, 8), (600, 128, 8), (300, 1024, 8), (5000, 16, 2)]
 
 
 @pytest.mark.parametrize("dt", (BF, F32))
