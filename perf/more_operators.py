@@ -333,8 +333,7 @@ def prepare(case, seed):
         if c["held"]:
             s["yq"], s["ys"] = held(rows * top_k, f)
     else:
-        # what the pairs return is not rounded before it is summed
-        s["y"], s["out"] = empty(rows * top_k, d, dtype=torch.float32), empty(rows, d)
+        s["y"], s["out"] = empty(rows * top_k, d), empty(rows, d)
         s["r"] = _hidden(g, rows, d, dt, 2.0) if c["residual"] else None
     if own:
         s["experts"] = _Experts(s["held"], d, k, _gated(c))
@@ -446,11 +445,11 @@ def _run_own(s):
     if c["op"] == "fused":
         lb.lora_mx_linear_fused(s["w"].at, *y, dt, *x, at(s["bias"]), act, at(s["r"]), c["d"], rows, st)
     else:
-        lb.lora_mx_expert_linear(s["experts"].at, s["plan"].at, *y, dt if c["op"] == "up" else lb.LORA_F32, *x,
+        lb.lora_mx_expert_linear(s["experts"].at, s["plan"].at, *y, dt, *x,
                                  lb.LORA_MOE_ROWS if c["op"] == "up" else lb.LORA_MOE_PAIRS, at(s["bias"]), act, st)
     if c["op"] == "down":
-        lb.lora_moe_combine(s["plan"].at, s["out"].data_ptr(), c["d"], s["y"].data_ptr(), c["d"], lb.LORA_F32, s["w"].data_ptr(),
-                            at(s["r"]), c["d"], dt, c["d"], st)
+        lb.lora_moe_combine(s["plan"].at, s["out"].data_ptr(), c["d"], s["y"].data_ptr(), c["d"], s["w"].data_ptr(), at(s["r"]),
+                            c["d"], dt, c["d"], st)
         return s["out"]
     if c["held"]:
         lb.lora_mx_dequantize(s["y"].data_ptr(), s["y"].stride(0), dt, *y[2:], lb.LORA_MX_E4M3, len(s["y"]), s["y"].shape[1], st)
