@@ -447,8 +447,11 @@ def lora_mx_expert_linear(x, plan, y: int, ldy: int, yq: int, ldyq: int, ys: int
 
 
 def lora_moe_combine(plan, out: int, ldo: int, y: int, ldy: int, y_dtype: int, weights: int,
-                     residual: int, ldr: int, dtype: int, d: int, stream=None):
-    """residual may be 0 (none)."""
+                     residual: int, ldr: int, dtype: int, d: int = None, stream=None):
+    """residual may be 0 (none).  y_dtype may be left out of a call by position, and y is then in
+    dtype: the weights' address, which is never 0 or 1, stands in its place."""
+    if y_dtype not in (LORA_F32, LORA_BF16):
+        y_dtype, weights, residual, ldr, dtype, d, stream = ldr, y_dtype, weights, residual, ldr, dtype, stream if d is None else d
     st = (_lib or load()).lora_moe_combine(plan, out, ldo, y, ldy, y_dtype, weights, residual, ldr, dtype, d, stream)
     if st:
         _check(st, "lora_moe_combine")
