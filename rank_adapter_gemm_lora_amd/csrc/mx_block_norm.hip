@@ -68,11 +68,12 @@ __device__ __forceinline__ float mx_odd_of(double v)
 // One row per workgroup of T threads, NU units of 8 elements a thread (unit t +
 // T j).  All of a row is loaded before anything is written, so outputs may
 // replace inputs.  Everything between the loads and the stores is in 64 bits
-// (the vector units run 64-bit products and sums at the 32-bit ones' rate; the
-// product of a bf16 weight and a bf16 gate is exact in 32): h and n then differ
-// from their exact values by some 2^-50, and each output is that value rounded
-// once.  Up to two units a thread the weights come with the row, ahead of the
-// sums; beyond, the registers would not hold them.
+// (the vector units run 64-bit products and sums at the 32-bit ones' rate): h and n
+// then differ from their exact values by some 2^-50, and each output is that value
+// rounded once.  A weight times a gate is exact there, where in fp32 it could leave
+// the range of both (35422 x 4096 with either: 318 us a pass).  Up to two units a
+// thread the weights come with the row, ahead of the sums; beyond, the registers
+// would not hold them.
 //
 // 35422 x 4096 bf16 with a channel's gate: 245 us, 1.31 GB at 5.3 TB/s, the vector
 // units issuing 73 % of the time (a pass with the blocks' inverse 322 us; weights
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
                 vpost[j].to_f32(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const double m = DT == DT_BF16 ? (double)(w[e] * g[e]) : (double)w[e] * (double)g[e];
+                    const double m = (double)w[e] * (double)g[e];
                     h[j][e] = fma(by * h[j][e], m, (double)r[e]);
                 }
             } else if (a.post || a.gate) {
