@@ -37,30 +37,62 @@ __device__ __forceinline__ void mx_load8(int dtype, const void *p, int64_t at, f
     }
 }
 
-// v / (1 + exp(-z)): exp as the hardware's power of two, with what its argument's
-// rounding loses brought in behind it, and the hardware's reciprocal; some five
-// roundings in all.  A denominator past 2^126 gives 0.
-__device__ __forceinline__ float mx_logistic_mul(float v, float z)
+// v times the logistic function of z, z of v's sign, from t + lost = -|z| log2(e), lost what
+// rounding t has left: with e = 2^(t + lost), max(v, -0) - |v| e / (1 + e).  The
+// power of two is the hardware's, with the lost part brought in behind it, the quotient
+// by the hardware's reciprocal and one correction by what is left of e.  Large values
+// are rounded once, at the end (v / (1 + e) would round 1 + e too, and the error's root mean
+// square over a product's results is then 5.0e-8 instead of 4.0e-8).  Under 2^-64, e and
+// with it the quotient are held times 2^64, so that neither leaves fp32 before the result
+// does (a SiLU of -87.4 is -1e-36).  Within 6 roundings, each operation counted at its worst.
+__device__ __forceinline__ float mx_times_logistic(float v, float t, float lost)
 {
-    constexpr float kLog2E = 1.44269504f, kLog2ELow = 1.925963033e-8f, kLn2 = 0.693147181f;
+#pragma clang fp contract(off)   // t + 64 joined to t's product would not have lost what is brought in
+    constexpr float kLn2 = 0.693147181f;
     constexpr int kPositive = 0x180;   // finite, not zero; the others stand
-    const float t = z * -kLog2E, lost = fmaf(z, -kLog2E, -t) - z * kLog2ELow;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return v * __builtin_amdgcn_rcpf(1.f + (__builtin_amdgcn_classf(e, kPositive) ? fmaf(e, lost * kLn2, e) : e));
+    const bool far = t < -64.f;
+    const float k = far ? 0x1p-64f : 1.f;
+    const float p = __builtin_amdgcn_exp2f(far ? t + 64.f : t);
+    const float e = __builtin_amdgcn_classf(p, kPositive) ? fmaf(p, lost * kLn2, p) : p;
+    const float d = fmaf(e, k, 1.f), rc = __builtin_amdgcn_rcpf(d), q = e * rc;
+    const float tail = fmaf(fmaf(-d, q, e), rc, q);
+    const float b = v > 0x1p100f ? 0x1p100f : fabsf(v);   // infinity has no tail: not infinity times 0
+    return fmaf(-(b * tail), k, v < 0.f ? -0.f : v);
 }
 
-// v Phi(v), Phi the normal distribution: with x = |v|, Phi(-x) = exp(-x^2 / 2) r(x),
-// r(x) = erfcx(x / sqrt 2) / 2, which falls slowly: a polynomial in 1 / (1 + 0.3 x),
-// fitted here to r on 0 <= x <= 14.5 by weighted least squares until its largest
-// relative error was least (5.8e-8).  Nothing cancels for negative v, as 1 + erf
-// would.  x^2's and its multiple's rounding are brought in behind the power of two.
-// Over all v within 8 roundings of the value (rms 1.3), in some 30 instructions
-// (512 x 4096 x 14336 with blocks 54.1 us; with the library's erfc, in branches over
-// its ranges, 56.9).
+// v / (1 + exp(-v))
+__device__ __forceinline__ float mx_silu(float v)
+{
+#pragma clang fp contract(off)
+    constexpr float kLog2E = 1.44269504f, kLog2ELow = 1.925963033e-8f;
+    const float x = fabsf(v), t = x * -kLog2E;
+    return mx_times_logistic(v, t, fmaf(-x, kLog2ELow, fmaf(x, -kLog2E, -t)));
+}
+
+// v (1 + tanh z) / 2, z = sqrt(2 / pi) (v + 0.044715 v^3), as v times the logistic function of
+// 2 z: the same expression without its cancellation, within 3 |2 z| roundings more for 2 z's
+// own (v^2, the sum of products and its constants; the product with |v| is brought in).
+__device__ __forceinline__ float mx_gelu_tanh(float v)
+{
+#pragma clang fp contract(off)
+    constexpr float kOne = -2.30220819f, kCube = -0.102943242f;   // -sqrt(8 / pi) log2(e), and 0.044715 times it
+    const float x = fabsf(v), w = fmaf(v * v, kCube, kOne), t = x * w;
+    return mx_times_logistic(v, t, fmaf(x, w, -t));
+}
+
+// v Phi(v), Phi the normal distribution: max(v, -0) - x Phi(-x) with x = |v|, and Phi(-x) =
+// exp(-x^2 / 2) r(x), r(x) = erfcx(x / sqrt 2) / 2, which falls slowly: a polynomial in
+// 1 / (1 + 0.3f x), fitted here to r on 0 <= x <= 13.3, where the power of two ends, by
+// weighted least squares until its largest relative error was least (5.9e-8 with the
+// coefficients as they are held).  Nothing cancels for negative v, as 1 + erf would, and
+// x r, near 0.4 where exp(-x^2 / 2) is smallest, keeps the tail's product normal as long as
+// the result is.  x^2's and its multiple's rounding are brought in behind the power of two.
+// Within 18 roundings, each operation counted at its worst (the polynomial's variable 3 at
+// a slope of 2.7, its sums 4.2, the power of two 3), for results from 2^-126 on.
 __device__ __forceinline__ float mx_gelu(float v)
 {
-    constexpr float kC[9] = {7.37266964e-06f, 0.119484201f, 0.121945299f, 0.0945857242f, 0.142765597f,
-                             -0.0768401325f, 0.228952199f, -0.169307664f, 0.0384074338f};
+    constexpr float kC[9] = {6.6857497e-06f, 0.1194959f, 0.12186197f, 0.09491117f, 0.14200212f,
+                             -0.07573549f, 0.2279869f, -0.16884065f, 0.03831141f};
     constexpr float kHalfLog2E = 0.721347511f, kHalfLog2ELow = 9.62981517e-9f, kLn2 = 0.693147181f;
     constexpr int kPositive = 0x180;   // finite, not zero; the others stand
     const float x = fabsf(v), t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.f));
@@ -70,13 +102,13 @@ __device__ __forceinline__ float mx_gelu(float v)
         r = fmaf(r, t, kC[i]);
     const float s = x * x, low = fmaf(x, x, -s), a = s * -kHalfLog2E;
     const float lost = fmaf(s, -kHalfLog2E, -a) - fmaf(low, kHalfLog2E, s * kHalfLog2ELow);
-    const float e = __builtin_amdgcn_exp2f(a);
-    const float below = r * (__builtin_amdgcn_classf(e, kPositive) ? fmaf(e, lost * kLn2, e) : e);   // Phi(-x)
-    return v * (v < 0.f ? below : 1.f - below);
+    const float p = __builtin_amdgcn_exp2f(a);
+    const float e = __builtin_amdgcn_classf(p, kPositive) ? fmaf(p, lost * kLn2, p) : p;
+    const float b = v > 0x1p100f ? 0x1p100f : x;   // infinity has no tail: not infinity times 0
+    return fmaf(-(b * r), e, v < 0.f ? -0.f : v);
 }
 
-// Activations in fp32.  The tanh form of GELU as v / (1 + exp(-2 z)), the same
-// expression without its cancellation.
+// Activations in fp32.
 __device__ __forceinline__ void mx_activate(int act, float (&f)[8])
 {
     if (act == LORA_ACT_RELU) {
@@ -86,7 +118,7 @@ __device__ __forceinline__ void mx_activate(int act, float (&f)[8])
     } else if (act == LORA_ACT_SILU) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = mx_logistic_mul(f[e], f[e]);
+            f[e] = mx_silu(f[e]);
     } else if (act == LORA_ACT_GELU) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -94,7 +126,7 @@ __device__ __forceinline__ void mx_activate(int act, float (&f)[8])
     } else if (act == LORA_ACT_GELU_TANH) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = mx_logistic_mul(f[e], 1.5957691216057308f * fmaf(0.044715f * f[e] * f[e], f[e], f[e]));
+            f[e] = mx_gelu_tanh(f[e]);
     }
 }
 
@@ -136,7 +168,7 @@ template <class JOB> struct MxFinish {
             if constexpr (JOB::kGated) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    f[e] = mx_logistic_mul(f[e], f[e]) * up[e];
+                    f[e] = mx_silu(f[e]) * up[e];
             } else {
                 mx_activate(job.act, f);
             }
