@@ -8,7 +8,10 @@ within one ulp, 2 u; second-order terms are under u / 1000 in all):
     what is left, so that its 5 u count 5 u at most there; the last sum u: 6 u.  The gate's product one more: 7 u.
   * gelu_tanh, the same with e = exp(-|2 z|): 2 z = v (a + b v^2) with v^2 and b u each, worth less than the whole, the sum of
     products and a u: 3 u of it, which is worth 3 |2 z| u where the logistic falls; 6 u as above.
-Results under 2^-126 are subnormal, or zero where the power of two itself is under 2^-126: 2^-126 there for
+  * gelu, v Phi(-x) with x = |v| and Phi(-x) = exp(-x^2 / 2) r(x): r's polynomial 1 u; its variable 1 / (1 + 0.3 x) 3 u, worth
+    |d log r / d log(1 / (1 + 0.3 x))| times as much, 2.7 at 0 and 1.24 at 13; its sums 4.2 u together, past x = 4 2.7 u;
+    times x u, the power of two 2 u and u, the last product and sum u.
+Results under 2^-126 are subnormal, or zero where the power of two itself is under 2^-126: 2^-126 there for gelu and
 gelu_tanh; silu's are rounded once more, to a multiple of 2^-149.
 """
 import numpy as np
@@ -82,6 +85,18 @@ def test_gelu_tanh():
         want = x / (1 + np.exp(-z2))
     fall = 1 / (1 + np.exp(np.minimum(z2, 700)))   # slope of log(1 + exp(-2 z))
     within(through(lb.LORA_ACT_GELU_TANH, v), want, 6.01 + 3 * np.abs(z2) * fall, np.where(np.abs(want) < 2.0 ** -126, 2.0 ** -126, 0.0))
+
+
+def test_gelu():
+    from scipy.special import erfcx, ndtr
+    note("gelu to its roundings")
+    v = values()
+    x = 0.0 + v.astype(np.float64)   # as above
+    want = x * ndtr(x)
+    size = np.minimum(np.abs(x), 20.0)
+    slope = (np.sqrt(2 / np.pi) / erfcx(size / np.sqrt(2)) - size) * (1 + 0.3 * size) / 0.3
+    within(through(lb.LORA_ACT_GELU, v), want, 6 + 3 * slope + np.where(size > 4, 2.7, 4.2),
+           np.where(np.abs(want) < 2.0 ** -126, 2.0 ** -126, 0.0))
 
 
 @pytest.mark.parametrize("rows", (1, 64))
