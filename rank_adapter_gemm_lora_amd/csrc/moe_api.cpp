@@ -156,10 +156,11 @@ lora_status lora_moe_combine(const lora_moe_plan *plan, void *out, int64_t ldo, 
         return LORA_E_ARG;
     if (plan->n_rows < 0)
         return LORA_E_EMPTY;
-    const int64_t n = plan->n_rows;
-    const lora_status st = check_shape(n, d, kMxMaxD);
-    if (st != LORA_OK)
-        return st;
+    const int64_t n = plan->n_rows;   // at most kMoeMaxPairs, which the plan has checked
+    if (d < 8 || d % 8 != 0)
+        return LORA_E_ARG;
+    if (d > kMxMaxD)
+        return LORA_E_UNSUPPORTED;
     if (!dense_ok(out, ldo, d, n) || !dense_ok(y, ldy, d, n * plan->top_k) ||
         (residual && !dense_ok(residual, ldr, d, n)) || (n > 0 && !aligned_to(weights, 4)))
         return LORA_E_ARG;
