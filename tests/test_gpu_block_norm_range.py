@@ -1,4 +1,4 @@
-"""lora_block_norm_mx with weights and gates far from one, whose product leaves fp32's range.
+"""lora_block_norm_mx with weights and gates far from one, whose product leaves fp32's range, and on another stream.
 
 The reference is the formula in 64 bits, which hold every product here; tolerances as in test_gpu_block_norm.py.  An
 output past its dtype's largest value is infinite, which the rounding of an exact value there gives too.
@@ -11,7 +11,7 @@ import mx_reference as R
 from gpu_helpers import note
 from rank_adapter_gemm_lora_amd import binding as lb
 from test_gpu_block_norm import FINE, call, near, reference
-from test_gpu_mx import BF, F32, blocks, check_blocks, dense, rand
+from test_gpu_mx import BF, F32, blocks, check_blocks, dense, rand, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,30 @@ def test_block_norm_weight_times_gate(weight, gate, scale, residual, dt, channel
         slack = np.where(eh != 0, FINE * size * np.abs(en / eh), FINE * np.abs(size * hn / np.sqrt((eh * eh).mean(-1, keepdims=True))))
     near(out.double().cpu().numpy(), en, dt, slack, "out")
     check_blocks(q.cpu().numpy(), s.cpu().numpy(), en, FINE, k)
+
+
+def test_block_norm_on_another_stream():
+    """Its bits on a stream of their own are those on the current one."""
+    rows, k = 40, 4096
+    y, _ = dense(rand(1, rows, k), BF)
+    r, _ = dense(rand(2, rows, k), BF)
+    w, _ = dense(rand(3, 1, k, 0.0), BF)
+    out, h = torch.empty_like(y), torch.empty_like(y)
+    q, s = blocks(rows, k, R.E4M3)
+    args = (rows, k, BF, y, r, w, w, 0, w, out, h, q, s)
+    note("block norm on another stream")
+    call(*args)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (out, h, q, s)]
+    for t in (out, h):
+        t.fill_(7.0)
+    for t in (q, s):
+        t[:rows].fill_(0)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        assert stream() == st.cuda_stream
+        call(*args)
+    st.synchronize()
+    for got, t in zip((out, h, q, s), want):
+        assert torch.equal(got, t)
