@@ -85,12 +85,19 @@ void experts_tiles(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g
 //     512   256       -          30.3         31.3            25.6             24.1
 // (top 2 of 8, 14336 -> 4096, mean 32: 32x64 66.7, 64x128 with k in 2 80.5).
 //
-// Beyond, 64x128; and from 1024 rows an expert on, in grids that stay full with
-// them, the larger tile (128x256, in 4 bits 128x128), whose unfilled tiles cost
-// more the fewer rows there are (top 8 of 64, 4096 -> 2 x 1024, 64x128 / larger):
-//     e4m3   2048 rows 217 / 266   4096 rows 386 / 399   8192 rows 749 / 728
-//     e2m1   1024 rows  88 /  96                         8192 rows 420 / 414
-// (1024 -> 4096 in fp32 with its combination, 8192 rows: 746 / 685).
+// Beyond, 64x128; and in grids that stay full with them the larger tile (128x256, in 4
+// bits 128x128), whose unfilled tiles cost more the fewer rows an expert has: from 512
+// rows an expert on, in 4 bits from 256 (64x128 / larger):
+//     mean                      256        384        512        640        768        1024       2048
+//     top 8 of 64, 4096 -> 2 x 1024
+//       e4m3                 212 / 221  294 / 291  377 / 371  466 / 454  550 / 536  721 / 694  1404 / 1354
+//       e2m1                 135 / 135  181 / 178  232 / 220  284 / 265  333 / 304  423 / 400   812 / 755
+//     top 8 of 64, 1024 -> 4096, fp32
+//       e4m3                 120 / 133  171 / 171  223 / 224  276 / 267  326 / 318  429 / 414   874 / 816
+//       e2m1                  84 /  80  114 / 108  146 / 137  181 / 169  215 / 198  283 / 266   554 / 505
+// and under eight of its workgroups a CU (e4m3, top 2 of 16; the last column has them):
+//     2048 -> 4096            53 /  68   76 /  86   98 / 107  120 / 125  144 / 149  190 / 192   371 / 364
+//     4096 -> 2 x 1024        59 /  81   81 /  84  102 / 124  122 / 125  144 / 154  186 / 199   354 / 352
 template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g, hipStream_t s)
 {
     const int64_t cu = a.n_cu, used = g.pairs < g.experts ? g.pairs : g.experts, mean = (g.pairs + used - 1) / used;
@@ -115,10 +122,10 @@ template <bool GATED, int FMT> void experts_pick(const MxLinearArgs &a, const Mx
     if (grid(64, 128) <= cu / 2)
         return experts_tiles<GATED, FMT, 4, 1, 1, 8, 2>(a, e, g, s);
     if constexpr (FMT == LORA_MX_E4M3) {
-        if (mean >= 1024 && grid(128, 256) >= 8 * cu)
+        if (mean >= 512 && grid(128, 256) >= 8 * cu)
             return experts_tiles<GATED, FMT, 2, 4, 2, 8, 1>(a, e, g, s);
     } else {
-        if (mean >= 1024 && grid(128, 128) >= 8 * cu)
+        if (mean >= 256 && grid(128, 128) >= 8 * cu)
             return experts_tiles<GATED, FMT, 8, 1, 1, 8, 1>(a, e, g, s);
     }
     experts_tiles<GATED, FMT, 4, 1, 1, 8, 1>(a, e, g, s);
