@@ -497,7 +497,8 @@ lora_status lora_mx_linear(const lora_mx_weight *w, void *y, int64_t ldy, lora_d
  * both.  bias: DEVICE [d], dtype, or NULL.  residual [n_rows][ldr], dtype, or
  * NULL; it may be y itself with the same stride.  act: relu v < 0 ? 0 : v; silu
  * v / (1 + exp(-v)); gelu v (1 + erf(v / sqrt 2)) / 2; gelu_tanh v (1 + tanh(sqrt(2 /
- * pi) (v + 0.044715 v^3))) / 2.  (LORA_ACT_SWIGLU is the experts' alone.)  Where
+ * pi) (v + 0.044715 v^3))) / 2; gelu's results under 2^-126 may be 0.
+ * (LORA_ACT_SWIGLU is the experts' alone.)  Where
  * adapters act on the product, they are added to y afterwards: an activation
  * belongs behind them (lora_swiglu_mx), bias and residual do not mind.  Otherwise
  * the outputs overlap nothing that is read.  Errors:
@@ -564,10 +565,11 @@ lora_status lora_swiglu_mx(void *out, int64_t ldo, void *q, int64_t ldq, void *s
  *      n = h * (mean_j h_j^2 + eps)^-1/2 * w_pre
  *      h_out = round(h),  out = round(n),  (q, s) = n in e4m3 blocks
  *
- * all in 64 bits, n from the unrounded h, each output rounded once.  w_post,
- * w_pre: DEVICE [k], dtype.  gate: DEVICE, dtype, [n_rows][ldg], or one row [k]
- * for all with ldg == 0.  out, h_out, and q with s may each be NULL, not all of
- * them; w_pre may be NULL if out and q are.  h_out and out may be y or residual
+ * all in 64 bits, n from the unrounded h, each output rounded once (bf16 and
+ * blocks under 2^-126 by way of fp32's multiples of 2^-149).  w_post, w_pre:
+ * DEVICE [k], dtype.  gate: DEVICE, dtype, [n_rows][ldg], or one row [k] for all
+ * with ldg == 0.  out, h_out, and q with s may each be NULL, not all of them;
+ * w_pre may be NULL if out and q are.  h_out and out may be y or residual
  * themselves with the same stride (in place); otherwise the outputs overlap
  * nothing.  eps >= 0, scale finite.  A row of zeros under a norm with eps == 0
  * gives NaN.  k <= 2^15.  Errors: LORA_E_ARG, LORA_E_UNSUPPORTED, LORA_E_HIP.
@@ -634,7 +636,7 @@ lora_status lora_moe_plan_destroy(lora_moe_plan *plan);
  *   offsets DEVICE int32 [n_experts + 1] or NULL: the first position of each
  *           group in that order; the last is the number of pairs with an expert
  *
- * order and offsets are copies: the plan keeps its own.  The launches depend on
+ * order is a copy: the plan keeps its own.  The launches depend on
  * sizes alone.  n_rows 0 .. max_rows.  Errors: LORA_E_ARG, LORA_E_HIP.
  */
 lora_status lora_moe_route(lora_moe_plan *plan, int32_t *ids, float *weights, int32_t *order,
@@ -687,7 +689,8 @@ lora_status lora_mx_experts_load_packed(lora_mx_experts *x, int expert, const vo
  *          [n_rows], row(p) = pair / top_k; LORA_MOE_PAIRS: rows in grouped order
  *          [n_rows * top_k], row(p) = p
  *   bias   DEVICE [n_experts][d], dtype, or NULL
- *   act    for ungated weights as in lora_mx_linear_fused; for gated ones
+ *   act    for ungated weights as in lora_mx_linear_fused (where adapters act on
+ *          the pairs' results: none, and lora_swiglu_mx behind them); for gated ones
  *          LORA_ACT_SWIGLU: v = g / (1 + exp(-g)) * u of the sums (with bias) g
  *          and u, none of them rounded before
  *   y      [n_rows * top_k][ldy], f columns; yq with ys alike; y, or yq with ys,
@@ -714,7 +717,8 @@ lora_status lora_mx_expert_linear(const lora_mx_experts *x, const lora_moe_plan 
  * over the pairs that have an expert, in the order of j, in fp32, rounded once.
  *   y        [n_rows * top_k][ldy] in y_dtype, rows in the grouped order; rows of
  *            pairs without an expert are not read.  (In LORA_F32 the pairs'
- *            results are not rounded on their way, at twice a bf16 y's traffic.)
+ *            results are not rounded on their way, at twice a bf16 y's traffic;
+ *            in bf16 each of them is off by up to 2^-8 of itself when it is summed.)
  *   weights  DEVICE float [n_rows][top_k]
  *   residual [n_rows][ldr] or NULL (0); may be out itself with the same stride
  *            (out overlaps nothing else that is read)

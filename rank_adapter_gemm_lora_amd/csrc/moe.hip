@@ -15,9 +15,11 @@
 // and one launch (64 rows of 64 experts, top 8: 7.2 us, a chain of dependent
 // steps); others three: rows in chunks, each with its histogram; the
 // histograms' sums over the chunks ahead; the chunks' pairs to their places.
-// 35422 rows of 128 experts, top 8, bf16: 9.8 + 3.7 + 9.4 us, the first bound by its
+// 35422 rows of 128 experts, top 8, bf16: 9.8 + 3.7 + 9.2 us, the first bound by its
 // instructions (19 us with the maximum over unsorted keys), the last by scattered
-// writes of 4 bytes (four arrays where the caller wants the order too).
+// writes of 4 bytes (the order, twice where the caller wants it too; the pairs' places
+// are written in their own order).  Given ids, a call among others: 64 rows top 8 of
+// 64 4.4 us (with order and offsets 4.9), 256 rows 5.6, 35422 of 128 13.2 (15.6).
 #include "mx_device.h"
 #include "moe.h"
 

@@ -68,7 +68,9 @@ void experts_tiles(const MxLinearArgs &a, const MxEpilogue &e, const MxGroups &g
 //     192   24        -   81.3  77.1        66.4  69.8            72.4
 //     256   32        -   94.1  86.8        73.8  77.6            72.9
 //     320   40        -  111.3  99.3        86.1  87.7            78.6
-// (64 rows: 285 MB of weights at 6 TB/s; top 2 of 8, 4096 -> 2 x 14336, mean 32: 140
+// (64 rows, 285 MB of weights: 5.6 TB/s by the kernel taken, 16x64 of 4, and 6.2 by the
+// 32x64 beside it: up to a mean of 8 the rule takes 16x64, which these figures, of k =
+// 4096 in 8 bits alone, do not bear out there; top 2 of 8, 4096 -> 2 x 14336, mean 32: 140
 // and 107); and with k = 1024, two groups of four chunks, 1024 -> 4096:
 //     64    8         -   35.2  27.5        34.5  31.9            29.2
 //     128   16        -   47.3  34.2        41.0  36.8            32.1
