@@ -78,7 +78,9 @@ __device__ __forceinline__ float mx_odd_of(double v)
 // 35422 x 4096 bf16 with a channel's gate: 245 us, 1.31 GB at 5.3 TB/s, the vector
 // units issuing 73 % of the time (a pass with the blocks' inverse 322 us; weights
 // loaded where they are used 344, one unit of 512 threads 350, four of 128 327).
-// 1 x 4096: 3.7 us.
+// 1 x 4096: 3.7 us.  Rows past 16384 go over the 128 registers of a lane of 1024
+// threads: 28 bytes of each in bf16, 228 in fp32, are kept in scratch (a call of 64 x
+// 32768 15.9 and 46 us, of 64 x 16384 8.6 and 10.1).
 template <int DT, int NU, int T>
 __global__ __launch_bounds__(T) void block_norm_mx_kernel(MxBlockNormArgs a)
 {
