@@ -22,7 +22,7 @@ import mx_reference as R
 from gpu_helpers import note
 from rank_adapter_gemm_lora_amd import binding as lb
 from test_gpu_moe import Plan
-from test_gpu_mx import DEV, F32, blocks, held, make_weight, stream
+from test_gpu_mx import DEV, F32, held, make_weight, stream
 from test_gpu_mx_experts import Experts
 
 pytestmark = pytest.mark.gpu
